@@ -1,0 +1,492 @@
+"""What the training-side and INT8 operators of the layer are measured on.
+
+Each case is one pass through an operator as a program that uses the layer calls it:
+
+  sort      tokens into expert order: counts, offsets, the permutation and its inverse
+            from the selected experts, and the token rows copied to their experts' rows
+  combine   expert-order rows back to their tokens, the router's weights applied
+  backward  the gradients of a training step's routing: of the combine (expert rows and
+            weights), of the copy into expert order, and of the router's logits
+  linear    a product in 8-bit integers: activations quantized per token, weights held
+            quantized per channel
+  experts   the routed SwiGLU experts in 8-bit integers, from the selected experts and the
+            token rows to the layer's routed output
+
+With `own` false the operators are computed in elementary torch operations in 32 bits,
+rounded once at the end; with `own` true by the framework's calls.
+"""
+import math
+
+import torch
+
+own = False
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+SCALE = 2.5  # routed scaling factor of the XS.2 workloads
+
+
+# --------------------------------------------------------------------------- cases
+
+def listed():
+    return [
+        # a decode step's 64 sequences at the XS.2 widths: three dependent steps on little
+        # data, so latency is what counts
+        dict(name="sort_decode", op="sort", T=64, d=2048, E=256, k=8, dtype="bf16", pad=0,
+             masked=0.0, skew=0.0),
+        # a prefill batch at the XS.2 widths, experts of unequal popularity, one token in
+        # twenty padding
+        dict(name="sort_prefill", op="sort", T=32768, d=2048, E=256, k=8, dtype="bf16", pad=0,
+             masked=0.05, skew=0.25),
+        # the way back of the decode step
+        dict(name="combine_decode", op="combine", T=64, d=2048, E=256, k=8, dtype="bf16", pad=0,
+             masked=0.0, skew=0.0),
+        # the way back at the M.1 widths as configured: 16 experts per token
+        dict(name="combine_wide", op="combine", T=16384, d=4096, E=256, k=16, dtype="bf16", pad=0,
+             masked=0.0, skew=0.25),
+        # a training microbatch of one 4096-token sequence at the XS.2 widths
+        dict(name="backward_4k", op="backward", T=4096, d=2048, E=256, k=8, dtype="bf16", pad=0,
+             masked=0.0, skew=0.25),
+        # fp32 training of a small odd model: rows that are no whole number of 16-byte
+        # vectors apart, padding tokens
+        dict(name="backward_odd", op="backward", T=1777, d=1003, E=60, k=6, dtype="f32", pad=3,
+             masked=0.1, skew=0.25),
+        # a large training batch at the M.1 widths
+        dict(name="backward_wide", op="backward", T=16384, d=4096, E=256, k=16, dtype="bf16",
+             pad=0, masked=0.0, skew=0.25),
+        # the shared expert's gate and up projections for one token
+        dict(name="linear_token", op="linear", M=1, N=1024, K=2048, dtype="bf16"),
+        # sizes that no tile divides, fp16 activations
+        dict(name="linear_odd", op="linear", M=777, N=1111, K=1000, dtype="f16"),
+        # the M.1 shared expert's gate and up projections over a prefill batch
+        dict(name="linear_prefill", op="linear", M=16384, N=2048, K=4096, dtype="bf16"),
+        # the routed experts of a decode step: every expert's weights for a row or two each
+        dict(name="experts_decode", op="experts", T=64, d=2048, E=256, k=8, F=512, masked=0.0,
+             skew=0.0),
+        # the routed experts of a prefill batch
+        dict(name="experts_prefill", op="experts", T=32768, d=2048, E=256, k=8, F=512,
+             masked=0.0, skew=0.02),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["sort", "combine", "backward", "linear", "experts"])
+    if op == "linear":
+        while True:
+            c = dict(op=op, M=_log(rng, 1, 32768), N=_log(rng, 16, 8192), K=_log(rng, 16, 8192),
+                     dtype=rng.choice(list(DT)))
+            if c["M"] * c["N"] * c["K"] <= 16384 * 2048 * 4096:
+                return c
+    if op == "experts":
+        while True:
+            E = rng.choice([8, 16, 60, 64, 128, 256])
+            c = dict(op=op, T=_log(rng, 1, 32768), d=64 * rng.randint(2, 64), E=E,
+                     k=rng.randint(1, min(16, E)), F=64 * rng.randint(1, 16),
+                     masked=rng.choice([0.0, 0.1]), skew=rng.choice([0.0, 0.02, 0.05]))
+            if (c["T"] * c["k"] + 1.5 * E * math.sqrt(c["T"])) * c["F"] * c["d"] <= \
+                    32768 * 8 * 512 * 2048 and E * c["F"] * c["d"] <= 256 * 512 * 2048:
+                return c
+    while True:
+        E = rng.choice([8, 16, 60, 64, 128, 256, 512])
+        dtype = rng.choice(list(DT))
+        c = dict(op=op, T=_log(rng, 1, 32768), d=rng.choice([_log(rng, 64, 8192),
+                                                             64 * rng.randint(1, 128)]),
+                 E=E, k=rng.randint(1, min(16, E)), dtype=dtype, pad=rng.choice([0, 0, 1, 8]),
+                 masked=rng.choice([0.0, 0.0, 0.1, 0.5]), skew=rng.choice([0.0, 0.25]))
+        if c["T"] * c["k"] * c["d"] * (2 if dtype == "f32" else 1) <= 16384 * 16 * 4096:
+            return c
+
+
+# --------------------------------------------------------------------------- inputs
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _rows(g, rows, cols, pad, dtype):
+    """[rows, cols] of standard normal values, rows `cols + pad` elements apart."""
+    t = torch.empty(rows, cols + pad, dtype=dtype, device="cuda")
+    step = max(1, (1 << 27) // max(1, cols + pad))
+    for r in range(0, rows, step):
+        t[r:r + step] = _randn(g, min(step, rows - r), cols + pad).to(dtype)
+    return t[:, :cols]
+
+
+def _routing(c, g):
+    """A sigmoid router's logits [T, E] with experts of unequal popularity, the selected
+    experts and weights of each token, and the ids with padding tokens not routed."""
+    T, E, k = c["T"], c["E"], c["k"]
+    rank = 1 + torch.randperm(E, generator=g, device="cuda")
+    logits = _randn(g, T, E) - c["skew"] * 1.1 * torch.log(rank.float())
+    idx = torch.topk(logits, k, dim=1).indices
+    s = torch.sigmoid(torch.gather(logits, 1, idx))
+    w = s / s.sum(1, keepdim=True)
+    if c["masked"]:
+        off = torch.rand(T, 1, generator=g, device="cuda") < c["masked"]
+        idx = torch.where(off, -1, idx)
+        w = torch.where(off, 0.0, w)
+    return logits, idx.to(torch.int32).contiguous(), w.contiguous()
+
+
+def _order(idx, E):
+    """counts, offsets, perm and inverse of the stable expert order (perm padded with 0)."""
+    n = idx.numel()
+    e = idx.reshape(-1).long()
+    key = torch.where(e < 0, E, e)
+    order = torch.argsort(key, stable=True)
+    counts = torch.zeros(E + 1, dtype=torch.long, device=e.device)
+    counts.scatter_add_(0, key, torch.ones_like(key))
+    offsets = torch.cat([torch.zeros_like(counts[:1]), torch.cumsum(counts[:E], 0)])
+    row = torch.arange(n, device=e.device)
+    routed = row < offsets[E]
+    perm = torch.where(routed, order, 0)
+    inv = torch.empty_like(row).scatter_(0, order, torch.where(routed, row, -1))
+    return counts[:E].int(), offsets.int(), perm.int(), inv.int().reshape(idx.shape)
+
+
+def _quantized(w):
+    """int8 codes and scales of the rows of a float32 matrix (the model-load step)."""
+    s = w.abs().amax(-1, keepdim=True) / 127
+    s = torch.where(s == 0, 1.0, s)
+    return torch.round(w * (1.0 / s)).to(torch.int8), s[..., 0].contiguous()
+
+
+def _pitched(q):
+    """The same codes in rows a multiple of 16 bytes apart."""
+    K = q.shape[-1]
+    t = torch.zeros(*q.shape[:-1], (K + 15) // 16 * 16, dtype=torch.int8, device=q.device)
+    t[..., :K] = q
+    return t[..., :K]
+
+
+def prepare(case, seed):
+    c = dict(case)
+    g = _gen(seed)
+    s = {"c": c}
+    if c["op"] == "linear":
+        s["x"] = _rows(g, c["M"], c["K"], 0, DT[c["dtype"]])
+        q, s["w_scale"] = _quantized(_randn(g, c["N"], c["K"]) * 0.02)
+        s["w"] = _pitched(q)
+        return s
+    if c["op"] == "experts":
+        T, d, E, F = c["T"], c["d"], c["E"], c["F"]
+        _, s["idx"], s["w"] = _routing(c, g)
+        s["x"] = _rows(g, T, d, 0, torch.bfloat16)
+        s["gu"] = torch.empty(E, 2 * F, d, dtype=torch.int8, device="cuda")
+        s["dn"] = torch.empty(E, d, F, dtype=torch.int8, device="cuda")
+        s["gu_scale"] = torch.empty(E, 2 * F, device="cuda")
+        s["dn_scale"] = torch.empty(E, d, device="cuda")
+        for e in range(0, E, 32):
+            n = min(32, E - e)
+            s["gu"][e:e + n], s["gu_scale"][e:e + n] = _quantized(_randn(g, n, 2 * F, d) * 0.02)
+            s["dn"][e:e + n], s["dn_scale"][e:e + n] = _quantized(_randn(g, n, d, F) * 0.02)
+        # the most rows that an expert has: what a padded batch of products is sized by
+        s["cap"] = max(1, int(_order(s["idx"], E)[0].max()))
+        return s
+    T, d, E, k, pad, dt = c["T"], c["d"], c["E"], c["k"], c["pad"], DT[c["dtype"]]
+    s["logits"], s["idx"], s["w"] = _routing(c, g)
+    if c["op"] == "sort":
+        s["x"] = _rows(g, T, d, pad, dt)
+        return s
+    s["inv"] = _order(s["idx"], E)[3]
+    s["o"] = _rows(g, T * k, d, pad, dt)
+    if c["op"] == "combine":
+        s["shared"] = _rows(g, T, d, pad, dt)
+        return s
+    s["dy"] = _rows(g, T, d, pad, dt)
+    s["dxp"] = _rows(g, T * k, d, pad, dt)
+    return s
+
+
+# --------------------------------------------------------------------------- plain forms
+
+def _to_tokens(rows, inv, weight):
+    """sum_j weight[t, j] rows[inv[t, j]] in float32; slots that are not routed add nothing."""
+    live = inv >= 0
+    r = rows[torch.where(live, inv, 0).long()].float()
+    r = torch.where(live[..., None], r, 0.0)
+    return (r * weight[..., None]).sum(1) if weight is not None else r.sum(1)
+
+
+def _plain_sort(s):
+    c = s["c"]
+    counts, offsets, perm, inv = _order(s["idx"], c["E"])
+    routed = torch.arange(perm.numel(), device="cuda") < offsets[c["E"]]
+    x_perm = torch.where(routed[:, None], s["x"][(perm // c["k"]).long()], 0)
+    return {"counts": counts, "offsets": offsets, "perm": perm, "inv": inv, "x_perm": x_perm}
+
+
+def _plain_combine(s):
+    y = SCALE * _to_tokens(s["o"], s["inv"], s["w"]) + s["shared"].float()
+    return {"y": y.to(s["o"].dtype)}
+
+
+def _plain_backward(s):
+    c, inv, w, dt = s["c"], s["inv"], s["w"], s["o"].dtype
+    live = inv >= 0
+    row = torch.where(live, inv, 0).long()
+    dy = s["dy"].float()
+    # combine: d_o = scale w dy, d_w = scale <dy, o>
+    d_w = SCALE * (s["o"][row].float() * dy[:, None]).sum(-1)
+    d_w = torch.where(live, d_w, 0.0)
+    n = inv.numel()
+    d_o = torch.zeros(n + 1, c["d"], dtype=dt, device="cuda")  # the last row takes the rest
+    d_o[torch.where(live, inv, n).long()] = (SCALE * w[..., None] * dy[:, None]).to(dt)
+    # copy into expert order
+    dx = _to_tokens(s["dxp"], inv, None).to(dt)
+    # router: w_j = s_j / sum s, s = sigmoid(logit)
+    at = torch.where(live, s["idx"], 0).long()
+    l = torch.gather(s["logits"], 1, at)
+    sg = torch.sigmoid(l)
+    wn = sg / sg.sum(1, keepdim=True)
+    dl = wn * torch.sigmoid(-l) * (d_w - (d_w * wn).sum(1, keepdim=True))
+    d_logits = torch.zeros_like(s["logits"]).scatter_add_(1, at, torch.where(live, dl, 0.0))
+    return {"d_o": d_o[:n], "d_w": d_w, "dx": dx, "d_logits": d_logits}
+
+
+def _codes(x):
+    """Codes (as float32) and scales of rows quantized to 8 bits."""
+    # (divided by a tensor: by a plain number the quotient is not correctly rounded)
+    s = x.abs().amax(-1, keepdim=True) / torch.full((), 127.0, device=x.device)
+    s = torch.where(s == 0, 1.0, s)
+    return torch.round(x * (1.0 / s)), s
+
+
+def _plain_linear(s):
+    q, sx = _codes(s["x"].float())
+    y = (q @ s["w"].float().t()) * sx * s["w_scale"]
+    return {"y": y.to(s["x"].dtype)}
+
+
+def _plain_experts(s):
+    c = s["c"]
+    E, k, F, cap = c["E"], c["k"], c["F"], s["cap"]
+    _, offsets, perm, inv = _order(s["idx"], E)
+    # expert-order rows in a batch of E matrices of `cap` rows
+    row = torch.arange(perm.numel(), device="cuda")
+    e = torch.clamp(torch.searchsorted(offsets[1:], row.int(), right=True), max=E - 1)
+    routed = row < offsets[E]
+    at = torch.where(routed, e * cap + row - offsets[e], E * cap)
+    token = torch.where(routed, (perm // k).long(), c["T"])
+    src = torch.full((E * cap + 1,), c["T"], device="cuda").scatter_(0, at, token)[:-1]
+    x = torch.cat([s["x"].float(), torch.zeros(1, c["d"], device="cuda")])
+    q, sx = _codes(x)
+    z = torch.bmm(q[src].view(E, cap, -1), s["gu"].float().transpose(1, 2))
+    z = z * sx[src].view(E, cap, 1) * s["gu_scale"][:, None]
+    h = torch.nn.functional.silu(z[..., :F]) * z[..., F:]
+    q, sh = _codes(h)
+    o = torch.bmm(q, s["dn"].float().transpose(1, 2)) * sh * s["dn_scale"][:, None]
+    o = o.view(E * cap, -1)
+    place = torch.where(inv >= 0, at[torch.clamp(inv, min=0).long()], -1)
+    y = SCALE * _to_tokens(o, place, s["w"])
+    return {"y": y.to(torch.bfloat16)}
+
+
+# --------------------------------------------------------------------------- the framework
+
+def _kept(s):
+    """What a program keeps between calls: the binding, dims, workspace and output buffers."""
+    k = s.get("kept")
+    if k is None:
+        from sparse_moe_layer_select_b200 import moe as M
+        c = s["c"]
+        k = s["kept"] = {"M": M}
+        new = lambda *shape, dtype: torch.zeros(*shape, dtype=dtype, device="cuda")  # noqa: E731
+        i8 = lambda r, n: new(r, (n + 15) // 16 * 16, dtype=torch.int8)[:, :n]  # noqa: E731
+        if c["op"] == "linear":
+            k["ws"] = new(256, dtype=torch.uint8)
+            k["q"], k["s"] = i8(c["M"], c["K"]), new(c["M"], dtype=torch.float32)
+            k["y"] = new(c["M"], c["N"], dtype=s["x"].dtype)
+            return k
+        T, d, E, n = c["T"], c["d"], c["E"], c["T"] * c["k"]
+        k["dims"] = M.make_dims(T, d, E, c["k"], c.get("F", 0), 0, SCALE)
+        k["ws"] = M.alloc_sort_workspace(k["dims"])
+        k["r"] = M.alloc_sort(k["dims"])
+        for t in k["r"].values():
+            t.zero_()
+        if c["op"] == "experts":
+            F = c["F"]
+            k["xq"], k["xs"] = i8(n, d), new(n, dtype=torch.float32)
+            k["h"] = new(n, F, dtype=torch.float16)
+            k["hq"], k["hs"] = i8(n, F), new(n, dtype=torch.float32)
+            k["o"] = new(n, d, dtype=torch.float16)
+            k["y"] = new(T, d, dtype=torch.bfloat16)
+            return k
+        dt = DT[c["dtype"]]
+        rows = lambda r: new(r, d + c["pad"], dtype=dt)[:, :d]  # noqa: E731
+        if c["op"] == "sort":
+            k["x_perm"] = rows(n)
+        else:
+            k["y"] = rows(T)
+        if c["op"] == "backward":
+            k["d_o"] = rows(n)
+            k["d_w"] = new(T, c["k"], dtype=torch.float32)
+            k["d_logits"] = new(T, E, dtype=torch.float32)
+    return k
+
+
+def _own_sort(s):
+    k = _kept(s)
+    k["M"].sort(k["dims"], s["idx"], k["r"], k["ws"], x=s["x"], x_perm=k["x_perm"])
+    return {**k["r"], "x_perm": k["x_perm"]}
+
+
+def _own_combine(s):
+    k = _kept(s)
+    k["M"].combine(k["dims"], s["o"], s["inv"], s["w"], k["y"], shared=s["shared"])
+    return {"y": k["y"]}
+
+
+def _own_backward(s):
+    k = _kept(s)
+    M, dims = k["M"], k["dims"]
+    M.combine_backward(dims, s["dy"], s["o"], s["inv"], s["w"], k["d_o"], k["d_w"])
+    M.dispatch_backward(dims, s["dxp"], s["inv"], k["y"])
+    M.route_backward(dims, s["logits"], s["idx"], k["d_w"], k["d_logits"])
+    return {"d_o": k["d_o"], "d_w": k["d_w"], "dx": k["y"], "d_logits": k["d_logits"]}
+
+
+def _own_linear(s):
+    k = _kept(s)
+    k["M"].quantize_int8(s["x"], k["q"], k["s"])
+    k["M"].matmul_int8(k["q"], k["s"], s["w"], s["w_scale"], k["y"], k["ws"])
+    return {"y": k["y"]}
+
+
+def _own_experts(s):
+    k = _kept(s)
+    M, r, E = k["M"], k["r"], s["c"]["E"]
+    M.sort(k["dims"], s["idx"], r, k["ws"])
+    M.dispatch_int8(k["dims"], s["x"], r["inv"], k["xq"], k["xs"])
+    M.matmul_int8(k["xq"], k["xs"], s["gu"], s["gu_scale"], k["h"], k["ws"],
+                  offsets=r["offsets"], swiglu=True)
+    M.quantize_int8(k["h"], k["hq"], k["hs"], n_rows=r["offsets"][E:])
+    M.matmul_int8(k["hq"], k["hs"], s["dn"], s["dn_scale"], k["o"], k["ws"],
+                  offsets=r["offsets"])
+    M.combine(k["dims"], k["o"], r["inv"], s["w"], k["y"])
+    return {"y": k["y"]}
+
+
+def run(state):
+    op = state["c"]["op"]
+    if own:
+        return {"sort": _own_sort, "combine": _own_combine, "backward": _own_backward,
+                "linear": _own_linear, "experts": _own_experts}[op](state)
+    return {"sort": _plain_sort, "combine": _plain_combine, "backward": _plain_backward,
+            "linear": _plain_linear, "experts": _plain_experts}[op](state)
+
+
+# --------------------------------------------------------------------------- work
+
+def work(case):
+    c = case
+    if c["op"] == "linear":
+        es = DT[c["dtype"]].itemsize
+        M, N, K = c["M"], c["N"], c["K"]
+        return {"bytes": M * K * es + N * K + 4 * N + M * N * es, "flops": 2.0 * M * N * K}
+    T, d, E, k = c["T"], c["d"], c["E"], c["k"]
+    n = T * k
+    routed = n * (1 - c["masked"])
+    if c["op"] == "experts":
+        F = c["F"]
+        touched = E * (1 - (1 - min(1.0, k / E)) ** (T * (1 - c["masked"])))
+        return {"bytes": T * d * 2 + 8 * n + touched * (3 * F * d + 4 * (2 * F + d)) + T * d * 2,
+                "flops": 6.0 * routed * F * d}
+    es = DT[c["dtype"]].itemsize
+    if c["op"] == "sort":
+        return {"bytes": 4 * n + 4 * (2 * E + 1) + 4 * (routed + n) + (T + routed) * d * es,
+                "flops": 0}
+    if c["op"] == "combine":
+        return {"bytes": routed * d * es + 8 * n + 2 * T * d * es, "flops": 2.0 * routed * d}
+    return {"bytes": 3 * routed * d * es + 2 * T * d * es + 4 * n * 6 + 4 * T * E,
+            "flops": 4.0 * routed * d}
+
+
+# --------------------------------------------------------------------------- 64 bits
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    c = case
+    f64 = torch.float64
+    if c["op"] == "sort":
+        # copied rows have the values of x itself
+        T, d, k = c["T"], c["d"], c["k"]
+        if T * k * d > 1 << 29:
+            return None
+        pairs = sorted((e, p) for p, e in enumerate(s["idx"].reshape(-1).tolist()) if e >= 0)
+        out = torch.zeros(T * k, d, dtype=f64, device="cuda")
+        if pairs:
+            at = torch.tensor([p // k for _, p in pairs], device="cuda")
+            out[:len(pairs)] = s["x"].to(f64)[at]
+        return {"counts": None, "offsets": None, "perm": None, "inv": None, "x_perm": out}
+    if c["op"] == "linear":
+        q, sx = _codes64(s["x"])
+        return {"y": (q @ s["w"].to(f64).t()) * sx[:, None] * s["w_scale"].to(f64)[None]}
+    if c["op"] == "experts":
+        T, d, E, k, F = c["T"], c["d"], c["E"], c["k"], c["F"]
+        q, sx = _codes64(s["x"])
+        y = torch.zeros(T, d, dtype=f64, device="cuda")
+        for e in range(E):
+            t, j = torch.nonzero(s["idx"] == e, as_tuple=True)
+            if t.numel() == 0:
+                continue
+            z = (q[t] @ s["gu"][e].to(f64).t()) * sx[t, None] * s["gu_scale"][e].to(f64)
+            gate, up = z[:, :F], z[:, F:]
+            h = gate / (1 + torch.exp(-gate)) * up
+            a = h.abs().amax(1, keepdim=True) / 127
+            a[a == 0] = 1
+            o = (torch.round(h / a) @ s["dn"][e].to(f64).t()) * a * s["dn_scale"][e].to(f64)
+            y.index_add_(0, t, o * (SCALE * s["w"][t, j].to(f64))[:, None])
+        return {"y": y}
+    T, d, k, inv = c["T"], c["d"], c["k"], s["inv"].long()
+    if c["op"] == "combine":
+        y = s["shared"].to(f64)
+        for j in range(k):
+            on = inv[:, j] >= 0
+            y[on] += SCALE * s["w"][on, j, None].to(f64) * s["o"][inv[on, j]].to(f64)
+        return {"y": y}
+    dy = s["dy"].to(f64)
+    big = T * k * d > 1 << 30  # d_o in 64 bits would not leave room for the rest
+    d_o = None if big else torch.zeros(T * k, d, dtype=f64, device="cuda")
+    d_w = torch.zeros(T, k, dtype=f64, device="cuda")
+    dx = torch.zeros(T, d, dtype=f64, device="cuda")
+    for j in range(k):
+        on = inv[:, j] >= 0
+        r = inv[on, j]
+        if not big:
+            d_o[r] = SCALE * s["w"][on, j, None].to(f64) * dy[on]
+        d_w[on, j] = SCALE * (dy[on] * s["o"][r].to(f64)).sum(1)
+        dx[on] += s["dxp"][r].to(f64)
+    d_logits = torch.zeros(T, c["E"], dtype=f64, device="cuda")
+    on = (s["idx"] >= 0).all(1)
+    if bool(on.any()):
+        at = s["idx"][on].long()
+        l = torch.gather(s["logits"][on].to(f64), 1, at)
+        p = 1 / (1 + torch.exp(-l))
+        total = p.sum(1, keepdim=True)
+        # d(p_i / total) / dp_j = (i == j) / total - p_i / total^2
+        g = d_w[on] / total - (d_w[on] * p).sum(1, keepdim=True) / total ** 2
+        part = torch.zeros(at.shape[0], c["E"], dtype=f64, device="cuda")
+        part.scatter_(1, at, g * p * (1 - p))
+        d_logits[on] = part
+    return {"d_o": d_o, "d_w": d_w, "dx": dx, "d_logits": d_logits}
+
+
+def _codes64(x):
+    """The codes that the definition gives: each step one rounding to 32 bits."""
+    import numpy as np
+    a = x.float().cpu().numpy()
+    s = np.abs(a).max(1) / np.float32(127)
+    s = np.where(s == 0, np.float32(1), s).astype(np.float32)
+    q = np.rint(a * (np.float32(1) / s)[:, None])
+    return (torch.from_numpy(q).to("cuda", torch.float64),
+            torch.from_numpy(s).to("cuda", torch.float64))
