@@ -175,6 +175,56 @@ cudaError_t launch_bf16_to_f16(const uint16_t *src, size_t n, uint16_t *dst, int
                                cudaStream_t s);
 cudaError_t launch_selftest_wait(int *status, long long limit_cycles, cudaStream_t s);
 
+// Bytes of one element of a moe_dtype.
+inline int elem_size(int dtype) { return dtype == 2 ? 4 : 2; }  // 2: MOE_DTYPE_F32
+
+// Row kernels by the inverse permutation inv [T, k] (sorted_rows.cu); strides in
+// elements; status: the status word of a workspace header, or null.
+cudaError_t launch_dispatch(int dtype, const void *x, int64_t x_stride, const int32_t *inv, int T,
+                            int k, int d, void *x_perm, int64_t p_stride, int *status,
+                            cudaStream_t s);
+// y[t] = scale sum_j w[t, j] o[inv[t, j]] + add[t]; w null: sum_j o[inv[t, j]] + add[t].
+cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const void *add,
+                             int64_t add_stride, const int32_t *inv, const float *w, int T, int k,
+                             int d, float scale, int out_type, void *y, int64_t y_stride,
+                             int *status, cudaStream_t s);
+cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride, const void *o,
+                                    int64_t o_stride, const int32_t *inv, const float *w, int T,
+                                    int k, int d, float scale, void *d_o, int64_t do_stride,
+                                    float *d_w, int *status, cudaStream_t s);
+cudaError_t launch_route_backward(const float *logits, const int32_t *topk_idx, const float *d_w,
+                                  int T, int E, int k, int norm, float *d_logits, int *status,
+                                  cudaStream_t s);
+// int8 codes and fp32 scales of rows (int8_rows.cu); inv non-null: the codes of row t go to
+// rows inv[t, j] (codes and scales then have rows * k rows).
+cudaError_t launch_quantize_int8(int dtype, const void *x, int64_t x_stride, int rows,
+                                 const int32_t *n_valid, const int32_t *inv, int k, int d,
+                                 int8_t *codes, int64_t c_stride, float *scales, int *status,
+                                 cudaStream_t s);
+
+// Product of 8-bit integers (int8_gemm.cu).
+struct Int8GemmParams {
+  int *status;             // workspace header (status word)
+  const int32_t *offsets;  // [G + 1] first row of each group, or null (one group: all rows)
+  const float *sa;         // [M] row scales
+  const float *sb;         // [G * b_rows] channel scales
+  void *out;
+  int64_t out_stride;      // elements
+  int M, N, K, G;
+  int b_rows;              // rows of b per group: N, or 2 N (SwiGLU: gate, then up)
+  int n_ctiles;            // channel tiles (set by the launcher)
+};
+cudaError_t launch_int8_gemm(Int8GemmParams p, int out_type, bool swiglu, const void *a,
+                             int64_t a_stride, const void *b, int64_t b_stride, int sms,
+                             cudaStream_t s);
+
+// Per-device set-up on the current device (once) and its SM count (moe_api.cu).
+cudaError_t current_device_setup(int *sms);
+// 2-D uint8 tensor map of [rows, cols] with `stride` bytes between rows: boxes of
+// 128 bytes x box_rows, 128-byte swizzle, zero fill.
+bool encode_map_u8(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t stride,
+                   uint32_t box_rows);
+
 // Sets what moe_last_launch_count() reports on this host thread (entry points
 // implemented outside moe_api.cu).
 void set_last_launch_count(int n);

@@ -19,6 +19,7 @@ cudaError_t gemm_set_attributes();
 cudaError_t gemm_pair_set_attributes();
 cudaError_t gemm_pair_max_clusters(int *clusters);
 cudaError_t gemm_fused_set_attributes();
+cudaError_t int8_gemm_set_attributes();
 }
 
 namespace {
@@ -83,6 +84,8 @@ cudaError_t device_setup(int *sms) {
     e = gemm_pair_max_clusters(&g_pair_clusters[dev]);
     if (e != cudaSuccess) return e;
     e = gemm_fused_set_attributes();
+    if (e != cudaSuccess) return e;
+    e = int8_gemm_set_attributes();
     if (e != cudaSuccess) return e;
     g_attrs[dev] = true;
   }
@@ -383,6 +386,20 @@ moe_status forward_impl(const Dims &D, const moe_weights_t *w, const moe_fp8_wei
 namespace moe {
 // Launch accounting of entry points implemented in other files.
 void set_last_launch_count(int n) { g_last_launches = n; }
+
+cudaError_t current_device_setup(int *sms) { return device_setup(sms); }
+
+bool encode_map_u8(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t stride,
+                   uint32_t box_rows) {
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {stride};
+  cuuint32_t box[2] = {128, box_rows};
+  cuuint32_t es[2] = {1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 }  // namespace moe
 
 extern "C" {

@@ -1,0 +1,328 @@
+// sorted_rows.cu -- token rows to expert order and back, with the router's
+// weights, and the gradients of both and of the router's logits.
+//
+// With inv[t, j] the expert-order row of token t's slot j (-1: not routed):
+//
+//   dispatch           x_perm[inv[t, j], :] = x[t, :]
+//   dispatch backward  dx[t, :] = sum_j d_x_perm[inv[t, j], :]  (+ add[t, :])
+//   combine            y[t, :] = s sum_j w[t, j] o[inv[t, j], :]  (+ shared[t, :])
+//   combine backward   d_o[inv[t, j], :] = s w[t, j] dy[t, :]
+//                      d_w[t, j] = s <dy[t, :], o[inv[t, j], :]>
+//   route backward     with p = w normalised over the slots (w_j = sigmoid(l_j) /
+//                      sum_i sigmoid(l_i)):  dl_j = p_j sigmoid(-l_j) (dw_j - sum_i dw_i p_i);
+//                      not normalised:       dl_j = sigmoid(l_j) sigmoid(-l_j) dw_j
+//
+// All of them move far more bytes than they compute and are bound by HBM, at
+// small batches by latency.  They go by the inverse permutation, token by
+// token, so that each token row is read (or written) once and every sum runs
+// in slot order: the results do not depend on the launch.  Sums are held in
+// fp32 and rounded once.  An inv entry outside [-1, T k) is skipped and
+// reported, so no row index reaches memory unchecked.
+#include "kernels.h"
+#include "rows.cuh"
+#include "status.cuh"
+
+#include <initializer_list>
+#include <type_traits>
+#include <utility>
+
+namespace moe {
+
+namespace {
+
+using namespace rows;
+
+constexpr int kThreads = 256;
+
+// The expert-order row of a slot, or -1.
+__device__ __forceinline__ int checked_row(int r, int n, int *status) {
+  if (r >= 0 && r < n) return r;
+  if (r != kNotRouted) record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_INVERSE_ROW);
+  return -1;
+}
+
+// One thread per (token, chunk): one load, up to k stores.
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads)
+    dispatch_kernel(const T *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ inv,
+                    int n_tokens, int k, int d, int chunks, T *__restrict__ x_perm,
+                    int64_t p_stride, int *status) {
+  const int64_t total = static_cast<int64_t>(n_tokens) * chunks;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int t = static_cast<int>(i / chunks);
+    const int c = static_cast<int>(i - static_cast<int64_t>(t) * chunks);
+    const Chunk<T, N> v = load_chunk<T, N>(x + t * x_stride, c, d);
+    const int32_t *slots = inv + static_cast<int64_t>(t) * k;
+    for (int j = 0; j < k; ++j) {
+      const int r = checked_row(slots[j], n_tokens * k, status);
+      if (r >= 0) store_chunk<T, N>(x_perm + r * p_stride, c, d, v);
+    }
+  }
+}
+
+// One thread per (token, chunk): up to k loads, summed in slot order.  y may be add
+// itself: a chunk is read before the same thread overwrites it.
+template <typename TI, typename TO, int N, bool WEIGHTED>
+__global__ void __launch_bounds__(kThreads)
+    to_tokens_kernel(const TI *__restrict__ o, int64_t o_stride, const TI *add,
+                     int64_t add_stride, const int32_t *__restrict__ inv,
+                     const float *__restrict__ w, int n_tokens, int k, int d, int chunks,
+                     float scale, TO *y, int64_t y_stride, int *status) {
+  const int64_t total = static_cast<int64_t>(n_tokens) * chunks;
+  for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const int t = static_cast<int>(i / chunks);
+    const int c = static_cast<int>(i - static_cast<int64_t>(t) * chunks);
+    const int64_t s0 = static_cast<int64_t>(t) * k;
+    float acc[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[e] = 0.f;
+    for (int j = 0; j < k; ++j) {
+      const int r = checked_row(inv[s0 + j], n_tokens * k, status);
+      if (r < 0) continue;
+      const float wj = WEIGHTED ? w[s0 + j] : 1.f;
+      const Chunk<TI, N> v = load_chunk<TI, N>(o + r * o_stride, c, d);
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[e] = fmaf(wj, to_f32(v.v[e]), acc[e]);
+    }
+    Chunk<TI, N> a;
+    if (add != nullptr) a = load_chunk<TI, N>(add + t * add_stride, c, d);
+    Chunk<TO, N> out;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      float v = WEIGHTED ? scale * acc[e] : acc[e];
+      if (add != nullptr) v += to_f32(a.v[e]);
+      out.v[e] = from_f32<TO>(v);
+    }
+    store_chunk<TO, N>(y + t * y_stride, c, d, out);
+  }
+}
+
+// One warp per slot: the slot's d_o row and its dot product.  d_o may be o
+// itself: a chunk is read before the same lane overwrites it.
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads)
+    combine_backward_kernel(const T *__restrict__ dy, int64_t dy_stride, const T *o,
+                            int64_t o_stride, const int32_t *__restrict__ inv,
+                            const float *__restrict__ w, int n_slots, int k, int d, int chunks,
+                            float scale, T *d_o, int64_t do_stride, float *__restrict__ d_w,
+                            int *status) {
+  const int lane = threadIdx.x & 31;
+  const int warps = (gridDim.x * kThreads) >> 5;
+  for (int i = (blockIdx.x * kThreads + threadIdx.x) >> 5; i < n_slots; i += warps) {
+    const int r = checked_row(inv[i], n_slots, status);
+    if (r < 0) {
+      if (lane == 0) d_w[i] = 0.f;
+      continue;
+    }
+    const float g = scale * w[i];
+    const T *dy_row = dy + (i / k) * dy_stride;
+    const T *o_row = o + r * o_stride;
+    T *do_row = d_o + r * do_stride;
+    float dot = 0.f;
+    for (int c = lane; c < chunks; c += 32) {
+      const Chunk<T, N> a = load_chunk<T, N>(dy_row, c, d);
+      const Chunk<T, N> b = load_chunk<T, N>(o_row, c, d);
+      Chunk<T, N> out;
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const float f = to_f32(a.v[e]);
+        dot = fmaf(f, to_f32(b.v[e]), dot);
+        out.v[e] = from_f32<T>(g * f);
+      }
+      store_chunk<T, N>(do_row, c, d, out);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    if (lane == 0) d_w[i] = scale * dot;
+  }
+}
+
+// One warp per token.  The normalised weights are a softmax of log sigmoid(l)
+// over the slots, taken with its maximum out, so that a row whose scores all
+// underflow still has its weights.  The row of d_logits is written whole:
+// zeros, then the selected experts' entries (an expert that a row names twice
+// gets the sum).
+template <int VEC>
+__global__ void __launch_bounds__(kThreads)
+    route_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
+                          const float *__restrict__ d_w, int n_tokens, int E, int k, int norm,
+                          float *__restrict__ d_logits, int *status) {
+  const int lane = threadIdx.x & 31;
+  const int warps = (gridDim.x * kThreads) >> 5;
+  for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < n_tokens; t += warps) {
+    float *row = d_logits + static_cast<int64_t>(t) * E;
+    for (int e = lane * VEC; e < E; e += 32 * VEC) {
+      if (VEC == 4) *reinterpret_cast<float4 *>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
+      else row[e] = 0.f;
+    }
+    int e = kNotRouted;
+    if (lane < k) {
+      e = topk_idx[static_cast<int64_t>(t) * k + lane];
+      if (e < 0 || e >= E) {
+        if (e != kNotRouted) record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_PERMUTE_EXPERT_ID);
+        e = kNotRouted;
+      }
+    }
+    const bool on = e >= 0;
+    const float l = on ? logits[static_cast<int64_t>(t) * E + e] : 0.f;
+    const float g = on ? d_w[static_cast<int64_t>(t) * k + lane] : 0.f;
+    const float q = 1.f / (1.f + expf(l));  // sigmoid(-l)
+    float dl;
+    if (norm) {
+      const float ls = on ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : -INFINITY;
+      float m = ls;
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      float p = on ? expf(ls - m) : 0.f;
+      float sum = p, dot = p * g;
+#pragma unroll
+      for (int off = 8; off > 0; off >>= 1) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        dot += __shfl_xor_sync(0xffffffffu, dot, off);
+      }
+      p /= sum;
+      dl = p * q * (g - dot / sum);
+    } else {
+      dl = q / (1.f + expf(-l)) * g;
+    }
+    float total = 0.f;
+    for (int j = 0; j < k; ++j) {
+      const int ej = __shfl_sync(0xffffffffu, e, j);
+      const float dj = __shfl_sync(0xffffffffu, dl, j);
+      if (ej == e) total += dj;
+    }
+    __syncwarp();  // the row's zeros are written
+    if (on) row[e] = total;
+  }
+}
+
+int sm_count() {
+  static int cached[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int sms = (dev >= 0 && dev < 64) ? cached[dev] : 0;
+  if (sms == 0) {
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (dev >= 0 && dev < 64) cached[dev] = sms;
+  }
+  return sms;
+}
+
+// Blocks of kThreads for `work` threads, at most eight per SM (grid-stride loops).
+int blocks_for(int64_t work) {
+  const int64_t want = (work + kThreads - 1) / kThreads;
+  const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
+  return static_cast<int>(want < cap ? (want > 0 ? want : 1) : cap);
+}
+
+// Elements per chunk: 8 where every row starts on a 16-byte boundary, 2 where
+// row strides are even (rows then start on a boundary of two elements), else
+// one (the base pointers are 16-byte aligned by the callers' check).
+int chunk_elems(std::initializer_list<std::pair<int64_t, int>> strides) {
+  bool v8 = true, v2 = true;
+  for (const auto &s : strides) {
+    v8 = v8 && (s.first * elem_size(s.second)) % 16 == 0;
+    v2 = v2 && s.first % 2 == 0;
+  }
+  return v8 ? 8 : v2 ? 2 : 1;
+}
+
+template <typename F>
+cudaError_t by_type(int dtype, F &&f) {
+  switch (dtype) {
+    case MOE_DTYPE_BF16: return f(__nv_bfloat16());
+    case MOE_DTYPE_F16: return f(__half());
+    default: return f(float());
+  }
+}
+
+template <typename F>
+cudaError_t by_chunk(int n, F &&f) {
+  switch (n) {
+    case 8: return f(std::integral_constant<int, 8>());
+    case 2: return f(std::integral_constant<int, 2>());
+    default: return f(std::integral_constant<int, 1>());
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_dispatch(int dtype, const void *x, int64_t x_stride, const int32_t *inv, int T,
+                            int k, int d, void *x_perm, int64_t p_stride, int *status,
+                            cudaStream_t s) {
+  return by_type(dtype, [&](auto tag) {
+    using Ty = decltype(tag);
+    return by_chunk(chunk_elems({{x_stride, dtype}, {p_stride, dtype}}), [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const int chunks = (d + N - 1) / N;
+      dispatch_kernel<Ty, N><<<blocks_for(static_cast<int64_t>(T) * chunks), kThreads, 0, s>>>(
+          static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
+          p_stride, status);
+      return cudaGetLastError();
+    });
+  });
+}
+
+cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const void *add,
+                             int64_t add_stride, const int32_t *inv, const float *w, int T, int k,
+                             int d, float scale, int out_type, void *y, int64_t y_stride,
+                             int *status, cudaStream_t s) {
+  const int n_elems = chunk_elems(
+      {{o_stride, in_type}, {add ? add_stride : 0, in_type}, {y_stride, out_type}});
+  return by_type(in_type, [&](auto ti) {
+    return by_type(out_type, [&](auto to) {
+      return by_chunk(n_elems, [&](auto n) {
+        using TI = decltype(ti);
+        using TO = decltype(to);
+        constexpr int N = decltype(n)::value;
+        const int chunks = (d + N - 1) / N;
+        const int grid = blocks_for(static_cast<int64_t>(T) * chunks);
+        const TI *op = static_cast<const TI *>(o), *ap = static_cast<const TI *>(add);
+        TO *yp = static_cast<TO *>(y);
+        if (w != nullptr)
+          to_tokens_kernel<TI, TO, N, true><<<grid, kThreads, 0, s>>>(
+              op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
+        else
+          to_tokens_kernel<TI, TO, N, false><<<grid, kThreads, 0, s>>>(
+              op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
+        return cudaGetLastError();
+      });
+    });
+  });
+}
+
+cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride, const void *o,
+                                    int64_t o_stride, const int32_t *inv, const float *w, int T,
+                                    int k, int d, float scale, void *d_o, int64_t do_stride,
+                                    float *d_w, int *status, cudaStream_t s) {
+  const int n_elems = chunk_elems({{dy_stride, dtype}, {o_stride, dtype}, {do_stride, dtype}});
+  return by_type(dtype, [&](auto tag) {
+    using Ty = decltype(tag);
+    return by_chunk(n_elems, [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      const int chunks = (d + N - 1) / N;
+      combine_backward_kernel<Ty, N>
+          <<<blocks_for(static_cast<int64_t>(T) * k * 32), kThreads, 0, s>>>(
+              static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o), o_stride, inv, w,
+              T * k, k, d, chunks, scale, static_cast<Ty *>(d_o), do_stride, d_w, status);
+      return cudaGetLastError();
+    });
+  });
+}
+
+cudaError_t launch_route_backward(const float *logits, const int32_t *topk_idx, const float *d_w,
+                                  int T, int E, int k, int norm, float *d_logits, int *status,
+                                  cudaStream_t s) {
+  const int grid = blocks_for(static_cast<int64_t>(T) * 32);
+  if (E % 4 == 0)
+    route_backward_kernel<4><<<grid, kThreads, 0, s>>>(logits, topk_idx, d_w, T, E, k, norm,
+                                                       d_logits, status);
+  else
+    route_backward_kernel<1><<<grid, kThreads, 0, s>>>(logits, topk_idx, d_w, T, E, k, norm,
+                                                       d_logits, status);
+  return cudaGetLastError();
+}
+
+}  // namespace moe
