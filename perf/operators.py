@@ -316,7 +316,7 @@ def _kept(s):
         if c["op"] == "experts":
             F = c["F"]
             k["xq"], k["xs"] = i8(n, d), new(n, dtype=torch.float32)
-            k["h"] = new(n, F, dtype=torch.float16)
+            k["h"] = new(n, F, dtype=torch.float32)  # fp16 would move codes of its quantization
             k["hq"], k["hs"] = i8(n, F), new(n, dtype=torch.float32)
             k["o"] = new(n, d, dtype=torch.float16)
             k["y"] = new(T, d, dtype=torch.bfloat16)
