@@ -26,28 +26,29 @@ namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 256;
-constexpr int kRegChunks = 16;  // chunks a lane keeps: rows of up to 512 chunks are read once
-
-template <int N>
-struct alignas(N) Codes {
-  int8_t v[N];
-};
-
 template <typename T, int N>
 __device__ __forceinline__ uint32_t chunk_amax_bits(const Chunk<T, N> &c, uint32_t m) {
   // |v| >= 0 orders as its bits do, with infinity and then NaN above every finite value
 #pragma unroll
-  for (int e = 0; e < N; ++e) m = max(m, __float_as_uint(fabsf(to_f32(c.v[e]))));
+  for (int e = 0; e < N; ++e) m = max(m, __float_as_uint(fabsf(element(c, e))));
   return m;
 }
+
+// Codes of a chunk, four to a word, the first in the low byte.
+template <int N>
+struct Codes {
+  uint32_t w[(N + 3) / 4];
+};
 
 template <typename T, int N>
 __device__ __forceinline__ Codes<N> chunk_codes(const Chunk<T, N> &c, float r) {
   Codes<N> q;
 #pragma unroll
+  for (int i = 0; i < (N + 3) / 4; ++i) q.w[i] = 0;
+#pragma unroll
   for (int e = 0; e < N; ++e)
-    q.v[e] = static_cast<int8_t>(__float2int_rn(__fmul_rn(to_f32(c.v[e]), r)));
+    q.w[e / 4] |= (static_cast<uint32_t>(__float2int_rn(__fmul_rn(element(c, e), r))) & 0xffu)
+                  << (8 * (e & 3));
   return q;
 }
 
@@ -55,11 +56,16 @@ template <int N>
 __device__ __forceinline__ void store_codes(int8_t *row, int c, int d, const Codes<N> &q) {
   const int e0 = c * N;
   if (N == 1 || e0 + N <= d) {
-    *reinterpret_cast<Codes<N> *>(row + e0) = q;
+    if constexpr (N == 16) *reinterpret_cast<uint4 *>(row + e0) = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
+    else if constexpr (N == 8) *reinterpret_cast<uint2 *>(row + e0) = make_uint2(q.w[0], q.w[1]);
+    else if constexpr (N == 2) *reinterpret_cast<uint16_t *>(row + e0) = static_cast<uint16_t>(q.w[0]);
+    else row[e0] = static_cast<int8_t>(q.w[0]);
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (e0 + e < d) row[e0 + e] = q.v[e];
+    for (int e = 0; e < N; ++e) {
+      if (e0 + e >= d) break;
+      row[e0 + e] = static_cast<int8_t>(q.w[e / 4] >> (8 * (e & 3)));
+    }
   }
 }
 
@@ -78,101 +84,117 @@ __device__ __forceinline__ bool row_scale(uint32_t amax_bits, float *scale, floa
   return true;
 }
 
-// One warp per row; DISPATCH: the row's codes go to row inv[t * k + j] of each slot j.
-template <typename T, int N, bool DISPATCH>
-__global__ void __launch_bounds__(kThreads)
+// TPR threads per row, each holding up to R chunks of it; longer rows (KEEP false)
+// are read a second time for their codes.  DISPATCH: the row's codes go to row
+// inv[t * k + j] of each slot j.
+template <typename T, int N, int TPR, int R, bool KEEP, bool DISPATCH>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     quantize_kernel(const T *__restrict__ x, int64_t x_stride, int n_rows,
                     const int32_t *__restrict__ n_valid, const int32_t *__restrict__ inv, int k,
                     int d, int chunks, int8_t *__restrict__ codes, int64_t c_stride,
                     float *__restrict__ scales, int *status) {
-  const int lane = threadIdx.x & 31;
-  const int warps = (gridDim.x * kThreads) >> 5;
-  const int rows_in = n_valid != nullptr ? min(n_rows, *n_valid) : n_rows;
-  for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < rows_in; t += warps) {
-    const T *row = x + t * x_stride;
-    const bool keep = chunks <= 32 * kRegChunks;
-    Chunk<T, N> v[kRegChunks];
-    uint32_t m = 0;
-    if (keep) {
+  constexpr int kBlock = TPR < 128 ? 128 : TPR;
+  constexpr int kWarps = TPR / 32;
+  __shared__ uint32_t warp_max[kBlock / 32];
+  const int lane = threadIdx.x % TPR;
+  const int64_t t = blockIdx.x * static_cast<int64_t>(kBlock / TPR) + threadIdx.x / TPR;
+  // (threads of one row leave together, and a block of several warps per row has one row)
+  if (t >= n_rows || (n_valid != nullptr && t >= *n_valid)) return;
+  const T *row = x + t * x_stride;
+  Chunk<T, N> v[R];
+  uint32_t m = 0;
+  if (KEEP) {
 #pragma unroll
-      for (int i = 0; i < kRegChunks; ++i)
-        if (lane + 32 * i < chunks) v[i] = load_chunk<T, N>(row, lane + 32 * i, d);
+    for (int i = 0; i < R; ++i)
+      if (lane + TPR * i < chunks) v[i] = load_chunk<T, N>(row, lane + TPR * i, d);
 #pragma unroll
-      for (int i = 0; i < kRegChunks; ++i)
-        if (lane + 32 * i < chunks) m = chunk_amax_bits(v[i], m);
-    } else {
-      for (int c = lane; c < chunks; c += 32) m = chunk_amax_bits(load_chunk<T, N>(row, c, d), m);
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    float scale, rcp;
-    const bool finite = row_scale(m, &scale, &rcp);
-    auto put = [&](int c, const Chunk<T, N> &val) {
-      Codes<N> q;
-      if (finite) {
-        q = chunk_codes(val, rcp);
-      } else {
+    for (int i = 0; i < R; ++i)
+      if (lane + TPR * i < chunks) m = chunk_amax_bits(v[i], m);
+  } else {
+    for (int c = lane; c < chunks; c += TPR) m = chunk_amax_bits(load_chunk<T, N>(row, c, d), m);
+  }
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (kWarps > 1) {
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+    __syncthreads();
+    m = __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? warp_max[threadIdx.x & 31] : 0);
+  }
+  float scale, rcp;
+  const bool finite = row_scale(m, &scale, &rcp);
+  auto put = [&](int c, const Chunk<T, N> &val) {
+    Codes<N> q = chunk_codes(val, rcp);
+    if (!finite) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) q.v[e] = 0;
-      }
-      if (!DISPATCH) {
-        store_codes<N>(codes + t * c_stride, c, d, q);
-      } else {
-        for (int j = 0; j < k; ++j) {
-          const int r = inv[static_cast<int64_t>(t) * k + j];
-          if (r >= 0 && r < n_rows * k)
-            store_codes<N>(codes + r * c_stride, c, d, q);
-        }
-      }
-    };
-    if (keep) {
-#pragma unroll
-      for (int i = 0; i < kRegChunks; ++i)
-        if (lane + 32 * i < chunks) put(lane + 32 * i, v[i]);
-    } else {
-      for (int c = lane; c < chunks; c += 32) put(c, load_chunk<T, N>(row, c, d));
+      for (int i = 0; i < (N + 3) / 4; ++i) q.w[i] = 0;
     }
     if (!DISPATCH) {
-      if (lane == 0) scales[t] = scale;
-    } else if (lane < k) {
-      const int r = inv[static_cast<int64_t>(t) * k + lane];
-      if (r >= 0 && r < n_rows * k) scales[r] = scale;
-      else if (r != kNotRouted) record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_INVERSE_ROW);
+      store_codes<N>(codes + t * c_stride, c, d, q);
+    } else {
+      for (int j = 0; j < k; ++j) {
+        const int r = inv[t * k + j];
+        if (r >= 0 && r < n_rows * k) store_codes<N>(codes + r * c_stride, c, d, q);
+      }
     }
+  };
+  if (KEEP) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (lane + TPR * i < chunks) put(lane + TPR * i, v[i]);
+  } else {
+    for (int c = lane; c < chunks; c += TPR) put(c, load_chunk<T, N>(row, c, d));
+  }
+  if (!DISPATCH) {
+    if (lane == 0) scales[t] = scale;
+  } else if (lane < k) {
+    const int r = inv[t * k + lane];
+    if (r >= 0 && r < n_rows * k) scales[r] = scale;
+    else if (r != kNotRouted) record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_INVERSE_ROW);
   }
 }
 
-int blocks_for_rows(int rows) {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int want = (rows + kThreads / 32 - 1) / (kThreads / 32);
-  return want < sms * 8 ? want : sms * 8;
+template <typename T, int N, int TPR, int R, bool KEEP>
+cudaError_t launch_shape(const void *x, int64_t x_stride, int rows, const int32_t *n_valid,
+                         const int32_t *inv, int k, int d, int8_t *codes, int64_t c_stride,
+                         float *scales, int *status, cudaStream_t s) {
+  constexpr int kBlock = TPR < 128 ? 128 : TPR;
+  const int chunks = (d + N - 1) / N;
+  const unsigned grid = (rows + kBlock / TPR - 1) / (kBlock / TPR);
+  const T *xp = static_cast<const T *>(x);
+  if (inv != nullptr)
+    quantize_kernel<T, N, TPR, R, KEEP, true><<<grid, kBlock, 0, s>>>(
+        xp, x_stride, rows, n_valid, inv, k, d, chunks, codes, c_stride, scales, status);
+  else
+    quantize_kernel<T, N, TPR, R, KEEP, false><<<grid, kBlock, 0, s>>>(
+        xp, x_stride, rows, n_valid, inv, k, d, chunks, codes, c_stride, scales, status);
+  return cudaGetLastError();
 }
 
+// Threads per row by the row's chunks, so that a thread holds four chunks at most and
+// a short row does not leave most of a warp idle.
 template <typename T, int N>
 cudaError_t launch_typed(const void *x, int64_t x_stride, int rows, const int32_t *n_valid,
                          const int32_t *inv, int k, int d, int8_t *codes, int64_t c_stride,
                          float *scales, int *status, cudaStream_t s) {
   const int chunks = (d + N - 1) / N;
-  const int grid = blocks_for_rows(rows);
-  const T *xp = static_cast<const T *>(x);
-  if (inv != nullptr)
-    quantize_kernel<T, N, true><<<grid, kThreads, 0, s>>>(xp, x_stride, rows, n_valid, inv, k, d,
-                                                          chunks, codes, c_stride, scales, status);
-  else
-    quantize_kernel<T, N, false><<<grid, kThreads, 0, s>>>(xp, x_stride, rows, n_valid, inv, k, d,
-                                                           chunks, codes, c_stride, scales, status);
-  return cudaGetLastError();
+#define MOE_QUANTIZE(TPR, R, KEEP)                                                             \
+  launch_shape<T, N, TPR, R, KEEP>(x, x_stride, rows, n_valid, inv, k, d, codes, c_stride, scales, \
+                                   status, s)
+  if (chunks <= 32 * 2) return MOE_QUANTIZE(32, 2, true);
+  if (chunks <= 32 * 4) return MOE_QUANTIZE(32, 4, true);
+  if (chunks <= 128 * 4) return MOE_QUANTIZE(128, 4, true);
+  if (chunks <= 512 * 4) return MOE_QUANTIZE(512, 4, true);
+  return MOE_QUANTIZE(512, 1, false);
+#undef MOE_QUANTIZE
 }
 
 template <typename T>
 cudaError_t launch_by_chunk(const void *x, int64_t x_stride, int rows, const int32_t *n_valid,
                             const int32_t *inv, int k, int d, int8_t *codes, int64_t c_stride,
                             float *scales, int *status, cudaStream_t s) {
-  // rows that all start on a 16-byte boundary move in 8-element chunks (c_stride is a
-  // multiple of 16)
+  // rows that all start on a 16-byte boundary move in chunks of 32 bytes (c_stride is a
+  // multiple of 16, so their codes are stored 8 or 16 at a time)
   if ((x_stride * static_cast<int64_t>(sizeof(T))) % 16 == 0)
-    return launch_typed<T, 8>(x, x_stride, rows, n_valid, inv, k, d, codes, c_stride, scales,
+    return launch_typed<T, 32 / sizeof(T)>(x, x_stride, rows, n_valid, inv, k, d, codes, c_stride, scales,
                               status, s);
   if (x_stride % 2 == 0)
     return launch_typed<T, 2>(x, x_stride, rows, n_valid, inv, k, d, codes, c_stride, scales,

@@ -127,7 +127,7 @@ cudaError_t launch_router_cc(const uint16_t *x, const uint16_t *w_router, const 
                              float *logits, int T, int d, int E, int sms, cudaStream_t s);
 // Warp-per-token selection over the fp32 logits of every token.
 // Expert id of a (token, slot) pair that is not routed (a padding token).
-constexpr int kNotRouted = -1;
+constexpr int32_t kNotRouted = -1;
 
 // token_mask (optional, [T]): 0 = padding token, which gets kNotRouted ids
 // and zero weights.  bias: the logit bias (its float64 refinement adds it);

@@ -41,66 +41,116 @@ __device__ __forceinline__ int checked_row(int r, int n, int *status) {
   return -1;
 }
 
+// Token and chunk of item i of the T x chunks items (32-bit division where it will do).
+__device__ __forceinline__ bool item_of(int n_tokens, int chunks, int *t, int *c) {
+  const int64_t total = static_cast<int64_t>(n_tokens) * chunks;
+  const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
+  if (i >= total) return false;
+  if (total <= 0xffffffffLL) *t = static_cast<uint32_t>(i) / static_cast<uint32_t>(chunks);
+  else *t = static_cast<int>(i / chunks);
+  *c = static_cast<int>(i - static_cast<int64_t>(*t) * chunks);
+  return true;
+}
+
+// Slots whose rows a thread has in flight at once: 128 bytes of loads.
+template <typename T, int N>
+constexpr int kBatch = sizeof(T) * N * 16 <= 128 ? 16 : 128 / (sizeof(T) * N);
+
+// Entries [j0, j0 + B) of a token's k slots, four to a load where every token's slots
+// start on a 16-byte boundary; `none` past the last.
+template <int B, typename V>
+__device__ __forceinline__ void load_slots(const V *slots, int j0, int k, V none, V (&out)[B]) {
+  static_assert(sizeof(V) == 4, "four entries to 16 bytes");
+  if (B % 4 == 0 && k % 4 == 0) {
+#pragma unroll
+    for (int j = 0; j < B; j += 4) {
+      V four[4] = {none, none, none, none};
+      if (j0 + j < k) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(slots + j0 + j);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) four[q] = *reinterpret_cast<const V *>(&w[q]);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) out[(j + q) % B] = four[q];
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < B; ++j) out[j] = j0 + j < k ? slots[j0 + j] : none;
+  }
+}
+
 // One thread per (token, chunk): one load, up to k stores.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads)
     dispatch_kernel(const T *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ inv,
                     int n_tokens, int k, int d, int chunks, T *__restrict__ x_perm,
                     int64_t p_stride, int *status) {
-  const int64_t total = static_cast<int64_t>(n_tokens) * chunks;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int t = static_cast<int>(i / chunks);
-    const int c = static_cast<int>(i - static_cast<int64_t>(t) * chunks);
-    const Chunk<T, N> v = load_chunk<T, N>(x + t * x_stride, c, d);
-    const int32_t *slots = inv + static_cast<int64_t>(t) * k;
-    for (int j = 0; j < k; ++j) {
-      const int r = checked_row(slots[j], n_tokens * k, status);
-      if (r >= 0) store_chunk<T, N>(x_perm + r * p_stride, c, d, v);
-    }
+  int t, c;
+  if (!item_of(n_tokens, chunks, &t, &c)) return;
+  const Chunk<T, N> v = load_chunk<T, N>(x + t * x_stride, c, d);
+  const int32_t *slots = inv + static_cast<int64_t>(t) * k;
+  for (int j0 = 0; j0 < k; j0 += 8) {
+    int r[8];
+    load_slots(slots, j0, k, kNotRouted, r);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r[j] = checked_row(r[j], n_tokens * k, status);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (r[j] >= 0) store_chunk<T, N>(x_perm + r[j] * p_stride, c, d, v);
   }
 }
 
-// One thread per (token, chunk): up to k loads, summed in slot order.  y may be add
-// itself: a chunk is read before the same thread overwrites it.
+// One thread per (token, chunk): up to k loads, kBatch of them in flight, summed in
+// slot order.  y may be add itself: a chunk is read before the same thread
+// overwrites it.
 template <typename TI, typename TO, int N, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads)
     to_tokens_kernel(const TI *__restrict__ o, int64_t o_stride, const TI *add,
                      int64_t add_stride, const int32_t *__restrict__ inv,
                      const float *__restrict__ w, int n_tokens, int k, int d, int chunks,
                      float scale, TO *y, int64_t y_stride, int *status) {
-  const int64_t total = static_cast<int64_t>(n_tokens) * chunks;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int t = static_cast<int>(i / chunks);
-    const int c = static_cast<int>(i - static_cast<int64_t>(t) * chunks);
-    const int64_t s0 = static_cast<int64_t>(t) * k;
-    float acc[N];
+  int t, c;
+  if (!item_of(n_tokens, chunks, &t, &c)) return;
+  constexpr int B = kBatch<TI, N>;
+  const int64_t s0 = static_cast<int64_t>(t) * k;
+  Chunk<TI, N> a;
+  if (add != nullptr) a = load_chunk<TI, N>(add + t * add_stride, c, d);
+  float acc[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) acc[e] = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int r = checked_row(inv[s0 + j], n_tokens * k, status);
-      if (r < 0) continue;
-      const float wj = WEIGHTED ? w[s0 + j] : 1.f;
-      const Chunk<TI, N> v = load_chunk<TI, N>(o + r * o_stride, c, d);
+  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+  for (int j0 = 0; j0 < k; j0 += B) {
+    int r[B];
+    float wj[B];
+    Chunk<TI, N> v[B];
+    load_slots(inv + s0, j0, k, kNotRouted, r);
 #pragma unroll
-      for (int e = 0; e < N; ++e) acc[e] = fmaf(wj, to_f32(v.v[e]), acc[e]);
+    for (int j = 0; j < B; ++j) {
+      r[j] = checked_row(r[j], n_tokens * k, status);
+      wj[j] = 1.f;
     }
-    Chunk<TI, N> a;
-    if (add != nullptr) a = load_chunk<TI, N>(add + t * add_stride, c, d);
-    Chunk<TO, N> out;
+    if (WEIGHTED) load_slots(w + s0, j0, k, 0.f, wj);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      float v = WEIGHTED ? scale * acc[e] : acc[e];
-      if (add != nullptr) v += to_f32(a.v[e]);
-      out.v[e] = from_f32<TO>(v);
-    }
-    store_chunk<TO, N>(y + t * y_stride, c, d, out);
+    for (int j = 0; j < B; ++j)
+      if (r[j] >= 0) v[j] = load_chunk<TI, N>(o + r[j] * o_stride, c, d);
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (r[j] >= 0) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) acc[e] = fmaf(wj[j], element(v[j], e), acc[e]);
+      }
   }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    if (WEIGHTED) acc[e] *= scale;
+    if (add != nullptr) acc[e] += element(a, e);
+  }
+  store_chunk<TO, N>(y + t * y_stride, c, d, rounded<TO, N>(acc));
 }
 
-// One warp per slot: the slot's d_o row and its dot product.  d_o may be o
-// itself: a chunk is read before the same lane overwrites it.
+// One warp per slot: the slot's d_o row and its dot product, kBatch / 2 chunks of
+// both rows in flight.  d_o may be o itself: a chunk is read before the same lane
+// overwrites it.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads)
     combine_backward_kernel(const T *__restrict__ dy, int64_t dy_stride, const T *o,
@@ -108,35 +158,45 @@ __global__ void __launch_bounds__(kThreads)
                             const float *__restrict__ w, int n_slots, int k, int d, int chunks,
                             float scale, T *d_o, int64_t do_stride, float *__restrict__ d_w,
                             int *status) {
+  constexpr int B = kBatch<T, N> / 2;
   const int lane = threadIdx.x & 31;
-  const int warps = (gridDim.x * kThreads) >> 5;
-  for (int i = (blockIdx.x * kThreads + threadIdx.x) >> 5; i < n_slots; i += warps) {
-    const int r = checked_row(inv[i], n_slots, status);
-    if (r < 0) {
-      if (lane == 0) d_w[i] = 0.f;
-      continue;
-    }
-    const float g = scale * w[i];
-    const T *dy_row = dy + (i / k) * dy_stride;
-    const T *o_row = o + r * o_stride;
-    T *do_row = d_o + r * do_stride;
-    float dot = 0.f;
-    for (int c = lane; c < chunks; c += 32) {
-      const Chunk<T, N> a = load_chunk<T, N>(dy_row, c, d);
-      const Chunk<T, N> b = load_chunk<T, N>(o_row, c, d);
-      Chunk<T, N> out;
-#pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float f = to_f32(a.v[e]);
-        dot = fmaf(f, to_f32(b.v[e]), dot);
-        out.v[e] = from_f32<T>(g * f);
-      }
-      store_chunk<T, N>(do_row, c, d, out);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-    if (lane == 0) d_w[i] = scale * dot;
+  const int64_t slot = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  if (slot >= n_slots) return;
+  const int i = static_cast<int>(slot);
+  const int r = checked_row(inv[i], n_slots, status);
+  if (r < 0) {
+    if (lane == 0) d_w[i] = 0.f;
+    return;
   }
+  const float g = scale * w[i];
+  const T *dy_row = dy + (i / k) * dy_stride;
+  const T *o_row = o + r * o_stride;
+  T *do_row = d_o + r * do_stride;
+  float dot = 0.f;
+  for (int c0 = lane; c0 < chunks; c0 += 32 * B) {
+    Chunk<T, N> a[B], b[B];
+#pragma unroll
+    for (int q = 0; q < B; ++q)
+      if (c0 + 32 * q < chunks) {
+        b[q] = load_chunk<T, N>(o_row, c0 + 32 * q, d);
+        a[q] = load_chunk<T, N>(dy_row, c0 + 32 * q, d);
+      }
+#pragma unroll
+    for (int q = 0; q < B; ++q)
+      if (c0 + 32 * q < chunks) {
+        float out[N];
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const float f = element(a[q], e);
+          dot = fmaf(f, element(b[q], e), dot);
+          out[e] = g * f;
+        }
+        store_chunk<T, N>(do_row, c0 + 32 * q, d, rounded<T, N>(out));
+      }
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+  if (lane == 0) d_w[i] = scale * dot;
 }
 
 // One warp per token.  The normalised weights are a softmax of log sigmoid(l)
@@ -210,6 +270,10 @@ int sm_count() {
   return sms;
 }
 
+unsigned all_blocks(int64_t threads) {
+  return static_cast<unsigned>((threads + kThreads - 1) / kThreads);
+}
+
 // Blocks of kThreads for `work` threads, at most eight per SM (grid-stride loops).
 int blocks_for(int64_t work) {
   const int64_t want = (work + kThreads - 1) / kThreads;
@@ -257,7 +321,7 @@ cudaError_t launch_dispatch(int dtype, const void *x, int64_t x_stride, const in
     return by_chunk(chunk_elems({{x_stride, dtype}, {p_stride, dtype}}), [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      dispatch_kernel<Ty, N><<<blocks_for(static_cast<int64_t>(T) * chunks), kThreads, 0, s>>>(
+      dispatch_kernel<Ty, N><<<all_blocks(static_cast<int64_t>(T) * chunks), kThreads, 0, s>>>(
           static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
           p_stride, status);
       return cudaGetLastError();
@@ -278,7 +342,7 @@ cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const
         using TO = decltype(to);
         constexpr int N = decltype(n)::value;
         const int chunks = (d + N - 1) / N;
-        const int grid = blocks_for(static_cast<int64_t>(T) * chunks);
+        const unsigned grid = all_blocks(static_cast<int64_t>(T) * chunks);
         const TI *op = static_cast<const TI *>(o), *ap = static_cast<const TI *>(add);
         TO *yp = static_cast<TO *>(y);
         if (w != nullptr)
@@ -304,7 +368,7 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
       combine_backward_kernel<Ty, N>
-          <<<blocks_for(static_cast<int64_t>(T) * k * 32), kThreads, 0, s>>>(
+          <<<all_blocks(static_cast<int64_t>(T) * k * 32), kThreads, 0, s>>>(
               static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o), o_stride, inv, w,
               T * k, k, d, chunks, scale, static_cast<Ty *>(d_o), do_stride, d_w, status);
       return cudaGetLastError();
