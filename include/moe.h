@@ -432,8 +432,8 @@ moe_status moe_dispatch_int8(const moe_dims_t *dims, int32_t dtype, const void *
  * r of group g: rows offsets[g] to offsets[g + 1] - 1 (expert order; a device
  * array), or all M rows where offsets is NULL and G = 1.  The integer sums are
  * exact.  Rows outside every group are not written.  Offsets that decrease or
- * leave [0, M] are clamped and recorded as MOE_ERR_DEVICE_BOUNDS, and so is a
- * finite result beyond the range of fp16 output.
+ * leave [0, M] are clamped and recorded as MOE_ERR_DEVICE_BOUNDS, and so is an
+ * infinite result in fp16 output (one beyond the type's range).
  * a: [M, K] int8, b: [G * N, K] int8 (2 N rows per group with MOE_INT8_SWIGLU), row
  * strides in bytes, multiples of 16; out: [M, N] of out_dtype, row stride in
  * elements.  Any N; K <= 131071; G <= 512.  ws needs only 256 bytes (status

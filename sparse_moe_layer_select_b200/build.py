@@ -1,7 +1,8 @@
-"""Build the two in-tree shared libraries with nvcc for sm_100a.
+"""Build the in-tree shared libraries (nvcc for sm_100a, the host compiler for the binding).
 
-  libmoe_b200.so  the MoE layer (C ABI of include/moe.h)
-  libmoe_gen.so   the seeded input generator (test and benchmark inputs only)
+  libmoe_b200.so    the MoE layer (C ABI of include/moe.h)
+  libmoe_gen.so     the seeded input generator (test and benchmark inputs only)
+  _rows_binding.so  argument marshalling of the row and 8-bit integer calls (CPython module)
 
 Usage: python -m sparse_moe_layer_select_b200.build   (or build() from Python)
 """
@@ -18,7 +19,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 MOE_SOURCES = ["moe_api.cu", "moe_gemm.cu", "moe_gemm_pair.cu", "moe_fused.cu", "router_cc.cu",
                "index.cu", "elementwise.cu", "permute_static.cu", "sorted_rows.cu", "int8_rows.cu",
-               "int8_gemm.cu", "rows_api.cu"]
+               "int8_gemm.cu", "int8_gemm_pair.cu", "rows_api.cu"]
 GEN_SOURCES = ["gen.cu"]
 
 
@@ -52,10 +53,37 @@ def _build_lib(name, sources, extra=(), force=False, verbose=False):
     return out
 
 
+def _build_binding(force=False, verbose=False):
+    """The CPython module over the C ABI (it reads torch tensors, so it needs torch's headers)."""
+    out = os.path.join(PKG, "_rows_binding.so")
+    src = os.path.join(CSRC, "rows_binding.cpp")
+    if not force and not _newer(out, [src, os.path.join(ROOT, "include", "moe.h")]):
+        return out
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    inc = [f"-I{d}" for d in cpp_extension.include_paths()]
+    inc += ["-I" + sysconfig.get_paths()["include"],
+            "-I" + os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    abi = int(torch.compiled_with_cxx11_abi())
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+           *inc, src, "-o", out + ".tmp", f"-L{PKG}", "-l:libmoe_b200.so", f"-L{lib}",
+           "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+           "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.run(cmd, check=True)
+    os.replace(out + ".tmp", out)
+    return out
+
+
 def build(force=False, verbose=False):
-    """Compile both libraries (skips up-to-date ones); returns their paths."""
+    """Compile the libraries (skips up-to-date ones); returns the paths of the first two."""
     moe = _build_lib("libmoe_b200.so", MOE_SOURCES, force=force, verbose=verbose)
     gen = _build_lib("libmoe_gen.so", GEN_SOURCES, force=force, verbose=verbose)
+    _build_binding(force=force, verbose=verbose)
     return moe, gen
 
 

@@ -23,21 +23,18 @@
 #include <algorithm>
 #include <type_traits>
 
-#include "kernels.h"
-#include "ptx.cuh"
-#include "rows.cuh"
-#include "status.cuh"
+#include "int8_common.cuh"
 
 namespace moe {
 
 namespace {
 
+using namespace int8;
+
 constexpr int kThreads = 192;
-constexpr int kMaxGroups = 512;
 constexpr int kTileChannels = 128;
 constexpr int kTileRows = 128;
 constexpr int kRowBox = 32;                  // rows of one TMA box of a
-constexpr int kStageK = 128;                 // one 128-byte swizzle row
 constexpr int kBBytes = kTileChannels * kStageK;
 constexpr int kABytes = kTileRows * kStageK;
 constexpr int kTmemCols = 512;
@@ -57,87 +54,6 @@ struct Smem {
 };
 static_assert(Smem<true>::total + 1024 <= 232448 && Smem<false>::total + 1024 <= 232448,
               "shared memory budget");
-
-// One tile of the output: up to kTileRows rows of a group by 128 channels.
-struct Work {
-  int group, row0, nrows, chan0;
-};
-
-// Running sums over the groups: first_tile[g] = tiles of the groups before g,
-// first_row[g] = their first row, clamped to [0, M] and made non-decreasing, so
-// that offsets that no sort wrote cannot lead outside the matrices.
-__device__ __forceinline__ void group_tiles(const Int8GemmParams &p, int tile_rows, int *first_tile,
-                                            int *first_row) {
-  const int lane = threadIdx.x & 31;
-  if (threadIdx.x < 32) {
-    int tiles = 0, top = 0;
-    for (int g0 = 0; g0 < p.G; g0 += 32) {
-      const int g = g0 + lane;
-      int lo = 0, hi = 0;
-      if (g < p.G) {
-        lo = p.offsets ? p.offsets[g] : 0;
-        hi = p.offsets ? p.offsets[g + 1] : p.M;
-      }
-      bool bad = g < p.G && (lo < 0 || hi < lo || hi > p.M);
-      lo = min(max(lo, 0), p.M);
-      hi = min(max(hi, 0), p.M);
-      // running maximum of the group ends: a group starts where the last one ended
-      int end = hi;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, end, off);
-        if (lane >= off) end = max(end, y);
-      }
-      end = max(end, top);
-      int start = __shfl_up_sync(0xffffffffu, end, 1);
-      if (lane == 0) start = top;
-      if (g == 0) start = lo;
-      start = min(max(start, lo), end);
-      int nt = g < p.G ? (end - start + tile_rows - 1) / tile_rows : 0;
-      int sum = nt;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, off);
-        if (lane >= off) sum += y;
-      }
-      if (g < p.G) {
-        first_tile[g] = tiles + sum - nt;
-        first_row[g] = start;
-      }
-      if (g == p.G - 1) first_row[p.G] = end;
-      tiles += __shfl_sync(0xffffffffu, sum, 31);
-      top = __shfl_sync(0xffffffffu, end, 31);
-      if (bad) record_status(p.status, MOE_ERR_DEVICE_BOUNDS, SITE_GROUP_OFFSETS);
-    }
-    if (lane == 0) first_tile[p.G] = tiles;
-  }
-}
-
-__device__ __forceinline__ Work find_work(const Int8GemmParams &p, int tile_rows, int item,
-                                          const int *first_tile, const int *first_row) {
-  const int ti = item / p.n_ctiles;
-  int lo = 0, hi = p.G - 1;  // the last group whose first tile is <= ti
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (first_tile[mid] <= ti) lo = mid;
-    else hi = mid - 1;
-  }
-  Work w;
-  w.group = lo;
-  w.row0 = first_row[lo] + (ti - first_tile[lo]) * tile_rows;
-  const int end = lo + 1 < p.G ? first_row[lo + 1] : first_row[p.G];
-  w.nrows = min(tile_rows, end - w.row0);
-  w.chan0 = (item - ti * p.n_ctiles) * kTileChannels;
-  return w;
-}
-
-__device__ __forceinline__ float silu(float g) { return g / (1.f + __expf(-g)); }
-
-template <typename TO>
-__device__ __forceinline__ TO rounded(float v, float *amax) {
-  *amax = fmaxf(*amax, fabsf(v));
-  return rows::from_f32<TO>(v);
-}
 
 template <typename TO, bool SWIGLU>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -190,11 +106,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t ph = 0;
       long long issued = 0;
+      int group = 0;
       bool ok = true;
       for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-        const Work w = find_work(p, kTileRows, item, first_tile, first_row);
+        const Work w = find_work(p, kTileRows, item, first_tile, first_row, group);
         const int boxes = (w.nrows + kRowBox - 1) / kRowBox;
-        const int brow = w.group * p.b_rows + w.chan0;
+        const int brow = w.group * p.b_rows + (w.ctile * kTileChannels);
         for (int kb = 0; kb < n_kb; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, p.status, SITE_GEMM_PRODUCER_EMPTY)) {
             ok = false;
@@ -226,9 +143,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
+      int group = 0;
       bool ok = true;
       for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-        const Work w = find_work(p, kTileRows, item, first_tile, first_row);
+        const Work w = find_work(p, kTileRows, item, first_tile, first_row, group);
         const uint32_t idesc = idesc_i8_s32(kTileChannels, (w.nrows + 15) / 16 * 16);
         if (!mbar_wait(&acc_empty[acc], aph ^ 1, p.status, SITE_GEMM_MMA_ACC_EMPTY)) break;
         tc_fence_after();
@@ -270,10 +188,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3;  // this warp's quarter of the accumulator's lanes
     int acc = 0;
     uint32_t aph = 0;
+    int group = 0;
     float amax = 0.f;
     for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-      const Work w = find_work(p, kTileRows, item, first_tile, first_row);
-      const int chan = w.chan0 + q * 32 + lane;
+      const Work w = find_work(p, kTileRows, item, first_tile, first_row, group);
+      const int chan = (w.ctile * kTileChannels) + q * 32 + lane;
       const bool on = chan < p.N;
       const float *sb = p.sb + static_cast<int64_t>(w.group) * p.b_rows + chan;
       const float sb0 = on ? sb[0] : 0.f;
@@ -293,7 +212,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float sa = __shfl_sync(0xffffffffu, sa_lane, i);
           float v = static_cast<float>(static_cast<int>(d0[i])) * sa * sb0;
           if (SWIGLU) v = silu(v) * (static_cast<float>(static_cast<int>(d1[i])) * sa * sb1);
-          if (on && c + i < w.nrows) out[(c + i) * p.out_stride] = rounded<TO>(v, &amax);
+          if (on && c + i < w.nrows) {
+            out[(c + i) * p.out_stride] = rows::from_f32<TO>(v);
+            amax = fmaxf(amax, fabsf(v));
+          }
         }
       }
       tc_fence_before();
@@ -304,8 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         aph ^= 1;
       }
     }
-    // (an infinity from an infinite scale, or NaN, is the caller's and is not reported)
-    if (std::is_same<TO, __half>::value && amax > 65504.f && amax < INFINITY)
+    if (std::is_same<TO, __half>::value && __half2float(__float2half_rn(amax)) == INFINITY)
       record_status(p.status, MOE_ERR_DEVICE_BOUNDS, SITE_H_FP16_RANGE);
   }
 

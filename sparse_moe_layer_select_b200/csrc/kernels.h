@@ -213,13 +213,25 @@ struct Int8GemmParams {
   int M, N, K, G;
   int b_rows;              // rows of b per group: N, or 2 N (SwiGLU: gate, then up)
   int n_ctiles;            // channel tiles (set by the launcher)
+  int tma_out;             // pair kernel: output rows are a multiple of 16 bytes apart
+  int tma_clips;           // and N channels are a multiple of 16 bytes
+  int ring, boxes;         // pair kernel: pipeline stages, output boxes per epilogue warp
 };
+// On CTA pairs; clusters: pairs that can be resident at once.
+cudaError_t launch_int8_pair(Int8GemmParams p, int out_type, bool swiglu, const void *a,
+                             int64_t a_stride, const void *b, int64_t b_stride, int clusters,
+                             cudaStream_t s);
 cudaError_t launch_int8_gemm(Int8GemmParams p, int out_type, bool swiglu, const void *a,
                              int64_t a_stride, const void *b, int64_t b_stride, int sms,
                              cudaStream_t s);
 
-// Per-device set-up on the current device (once) and its SM count (moe_api.cu).
-cudaError_t current_device_setup(int *sms);
+// Per-device set-up on the current device (once), its SM count and how many CTA pairs
+// can be resident at once (moe_api.cu).
+cudaError_t current_device_setup(int *sms, int *clusters);
+// Store map of a [rows, cols] matrix of a moe_dtype, `stride` elements between rows:
+// boxes of 64 bytes x 32 rows, 64-byte swizzle.
+bool encode_out_map(CUtensorMap *m, const void *ptr, int dtype, uint64_t rows, uint64_t cols,
+                    uint64_t stride);
 // 2-D uint8 tensor map of [rows, cols] with `stride` bytes between rows: boxes of
 // 128 bytes x box_rows, 128-byte swizzle, zero fill.
 bool encode_map_u8(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t stride,

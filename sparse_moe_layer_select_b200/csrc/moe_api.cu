@@ -20,6 +20,7 @@ cudaError_t gemm_pair_set_attributes();
 cudaError_t gemm_pair_max_clusters(int *clusters);
 cudaError_t gemm_fused_set_attributes();
 cudaError_t int8_gemm_set_attributes();
+cudaError_t int8_pair_set_attributes();
 }
 
 namespace {
@@ -86,6 +87,8 @@ cudaError_t device_setup(int *sms) {
     e = gemm_fused_set_attributes();
     if (e != cudaSuccess) return e;
     e = int8_gemm_set_attributes();
+    if (e != cudaSuccess) return e;
+    e = int8_pair_set_attributes();
     if (e != cudaSuccess) return e;
     g_attrs[dev] = true;
   }
@@ -387,7 +390,27 @@ namespace moe {
 // Launch accounting of entry points implemented in other files.
 void set_last_launch_count(int n) { g_last_launches = n; }
 
-cudaError_t current_device_setup(int *sms) { return device_setup(sms); }
+cudaError_t current_device_setup(int *sms, int *clusters) {
+  const cudaError_t e = device_setup(sms);
+  if (e == cudaSuccess) *clusters = std::min(pair_clusters(), *sms / 2);
+  return e;
+}
+
+bool encode_out_map(CUtensorMap *m, const void *ptr, int dtype, uint64_t rows, uint64_t cols,
+                    uint64_t stride) {
+  const uint64_t es = elem_size(dtype);
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {stride * es};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(64 / es), 32};
+  cuuint32_t ones[2] = {1, 1};
+  const CUtensorMapDataType type = dtype == MOE_DTYPE_BF16  ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : dtype == MOE_DTYPE_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                            : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  return g_encode(m, type, 2, const_cast<void *>(ptr), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool encode_map_u8(CUtensorMap *m, const void *ptr, uint64_t rows, uint64_t cols, uint64_t stride,
                    uint32_t box_rows) {

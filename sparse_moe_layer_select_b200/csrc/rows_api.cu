@@ -266,8 +266,8 @@ moe_status moe_matmul_int8(const moe_int8_matmul_t *m, void *ws, size_t ws_bytes
   if (ws == nullptr || check_header(ws) != MOE_OK) return MOE_ERR_INVALID_ARG;
   if (ws_bytes < sizeof(WsHeader)) return MOE_ERR_WORKSPACE_TOO_SMALL;
   set_last_launch_count(0);
-  int sms = 0;
-  if (current_device_setup(&sms) != cudaSuccess) return MOE_ERR_CUDA;
+  int sms = 0, clusters = 0;
+  if (current_device_setup(&sms, &clusters) != cudaSuccess) return MOE_ERR_CUDA;
   Int8GemmParams p{};
   p.status = static_cast<int *>(ws);
   p.offsets = m->offsets;
@@ -280,8 +280,17 @@ moe_status moe_matmul_int8(const moe_int8_matmul_t *m, void *ws, size_t ws_bytes
   p.K = m->K;
   p.G = m->G;
   p.b_rows = static_cast<int>(b_rows);
-  return launched(launch_int8_gemm(p, m->out_dtype, swiglu, m->a, m->a_stride, m->b, m->b_stride,
-                                   sms, static_cast<cudaStream_t>(stream)),
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // CTA pairs from 96 rows per group on.  us on 128-row tiles and on pairs, 256 groups:
+  // N = 2048, K = 512: 96 / 102 at 64 rows each, 121 / 98 at 96, 156 / 98 at 128, 444 / 189 at
+  // 512; SwiGLU, N = 512, K = 2048: 115 / 129 at 64, 119 / 131 at 96, 135 / 133 at 128, 307 /
+  // 277 at 512.  One group, N = 2048, K = 4096: 16 / 20 at 16 rows, 22 / 20 at 128, 64 / 33 at
+  // 4096.
+  const bool pairs = m->M >= int64_t(96) * m->G;
+  return launched(pairs ? launch_int8_pair(p, m->out_dtype, swiglu, m->a, m->a_stride, m->b,
+                                           m->b_stride, clusters, s)
+                        : launch_int8_gemm(p, m->out_dtype, swiglu, m->a, m->a_stride, m->b,
+                                           m->b_stride, sms, s),
                   1);
 }
 

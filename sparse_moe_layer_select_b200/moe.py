@@ -2,7 +2,8 @@
 
 Every step of the layer runs in the CUDA kernels of libmoe_b200.so; this
 module only turns torch tensors into device pointers and checks status
-codes.  There is no fallback: if the library is missing, importing the
+codes (through ctypes; the row and 8-bit integer calls through the compiled
+module _rows_binding).  There is no fallback: if the library is missing, importing the
 functions raises.
 """
 from __future__ import annotations
@@ -145,22 +146,8 @@ def lib():
         L.moe_logits_offset.argtypes = [D]
         L.moe_profile_next_forward.restype = ctypes.c_int
         L.moe_profile_next_forward.argtypes = [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int32]
-        I, S = ctypes.c_int32, ctypes.c_int64
-        Z = ctypes.c_size_t
-        L.moe_sort_workspace_size.restype = Z
+        L.moe_sort_workspace_size.restype = ctypes.c_size_t
         L.moe_sort_workspace_size.argtypes = [D]
-        for name, args in [("moe_sort", [D, P, P, P, P, P, I, P, S, P, S, P, Z, P]),
-                           ("moe_dispatch", [D, I, P, S, P, P, S, P, P]),
-                           ("moe_dispatch_backward", [D, I, P, S, P, P, S, I, P, S, P, P]),
-                           ("moe_combine", [D, I, P, S, P, P, P, S, I, P, S, P, P]),
-                           ("moe_combine_backward", [D, I, P, S, P, S, P, P, P, S, P, P, P]),
-                           ("moe_route_backward", [D, P, P, P, P, P, P]),
-                           ("moe_quantize_int8", [I, I, I, P, S, P, P, S, P, P]),
-                           ("moe_dispatch_int8", [D, I, P, S, P, P, S, P, P, P]),
-                           ("moe_matmul_int8", [ctypes.POINTER(moe_int8_matmul_t), P, Z, P])]:
-            fn = getattr(L, name)
-            fn.restype = ctypes.c_int
-            fn.argtypes = args
         _LIB = L
     return _LIB
 
@@ -362,71 +349,32 @@ def last_launch_count() -> int:
 
 
 # ---------------------------------------------------------------- rows and 8-bit products
-# The calls below take their types, sizes and strides from the tensors, so they check them:
-# a mismatch raises MoeError(MOE_ERR_INVALID_ARG) before anything is launched.
+# Types, sizes and strides are taken from the tensors (and checked) by the compiled module
+# _rows_binding: at decode sizes these calls take less time on the device than that takes in
+# Python.  An argument that does not fit raises MoeError(MOE_ERR_INVALID_ARG) before anything is
+# launched; every tensor has to be on the current device.
 
-def _bad(where, what):
-    return MoeError(MOE_ERR_INVALID_ARG, f"{where} ({what})")
-
-
-_DTYPE = {}
+_ROWS = None
 
 
-def _dtype(t, where, what):
-    if not _DTYPE:
-        import torch
-        _DTYPE.update({torch.bfloat16: MOE_DTYPE_BF16, torch.float16: MOE_DTYPE_F16,
-                       torch.float32: MOE_DTYPE_F32})
-    code = _DTYPE.get(t.dtype)
-    if code is None:
-        raise _bad(where, f"{what}: {t.dtype}")
-    return code
+def _rows():
+    """The compiled binding (raises if it has not been built)."""
+    global _ROWS
+    if _ROWS is None:
+        lib()
+        try:
+            from . import _rows_binding
+        except ImportError as e:
+            raise RuntimeError("binding not built (run python -m "
+                               f"sparse_moe_layer_select_b200.build): {e}") from e
+        _ROWS = _rows_binding
+    return _ROWS
 
 
-def _rows(t, rows, cols, where, what, dtype=None):
-    """Row stride of a [rows, cols] matrix of `dtype` whose rows are contiguous."""
-    shape = t.shape
-    if len(shape) != 2 or shape[0] != rows or shape[1] != cols:
-        raise _bad(where, f"{what}: shape {tuple(shape)}, expected {(rows, cols)}")
-    if dtype is not None and t.dtype != dtype:
-        raise _bad(where, f"{what}: {t.dtype}, expected {dtype}")
-    stride, inner = t.stride()
-    if inner != 1 and cols > 1:
-        raise _bad(where, f"{what}: elements of a row are not adjacent")
-    return stride if rows > 1 else (cols + 15) // 16 * 16  # a single row has no stride
-
-
-def _flat(t, n, dtype, where, what):
-    """Address of a contiguous tensor of n elements."""
-    m = t.numel()
-    if m != n or t.dtype != dtype or not t.is_contiguous():
-        raise _bad(where, f"{what}: {m} elements of {t.dtype}, expected {n} of {dtype}, contiguous")
-    return t.data_ptr()
-
-
-def _launch_on(stream, where, *tensors):
-    """The raw stream for a call on the current device, where every tensor has to be."""
-    import torch
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or dev < 0):
-            raise _bad(where, f"a tensor on {t.device}: every tensor has to be on one CUDA device")
-    if dev != torch.cuda.current_device():
-        raise _bad(where, f"tensors on cuda:{dev}, which is not the current device")
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
-
-
-def _optional(t):
-    return None if t is None else t.data_ptr()
-
-
-def _header(ws, where):
-    """Address of an optional status header (the first 256 bytes of a workspace)."""
-    if ws is None:
-        return None
-    if ws.numel() * ws.element_size() < 256:
-        raise _bad(where, "ws: fewer than 256 bytes")
-    return ws.data_ptr()
+def _raise(code, where):
+    if isinstance(code, str):  # an argument that does not fit
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{where} ({code})")
+    raise MoeError(code, where)
 
 
 def sort_workspace_size(dims) -> int:
@@ -453,112 +401,45 @@ def alloc_sort(dims, device="cuda"):
 def sort(dims, topk_idx, out, ws, x=None, x_perm=None, stream=None):
     """moe_sort into the buffers of alloc_sort; with x [T, d] and x_perm [T * k, d], the rows
     are copied to expert order too."""
-    import torch
-    W = "moe_sort"
-    T, k, E, d = dims.T, dims.num_experts_per_tok, dims.num_experts, dims.d_model
-    i32 = torch.int32
-    args = [_flat(topk_idx, T * k, i32, W, "topk_idx"), _flat(out["counts"], E, i32, W, "counts"),
-            _flat(out["offsets"], E + 1, i32, W, "offsets"),
-            _flat(out["perm"], T * k, i32, W, "perm"), _flat(out["inv"], T * k, i32, W, "inv")]
-    if (x is None) != (x_perm is None):
-        raise _bad(W, "x without x_perm, or x_perm without x")
-    rows = (MOE_DTYPE_BF16, None, d, None, d)
-    if x is not None:
-        rows = (_dtype(x, W, "x"), x.data_ptr(), _rows(x, T, d, W, "x"), x_perm.data_ptr(),
-                _rows(x_perm, T * k, d, W, "x_perm", x.dtype))
-    _check(lib().moe_sort(ctypes.byref(dims), *args, *rows, ws.data_ptr(), ws.numel(),
-        _launch_on(stream, W, topk_idx, *out.values(), x, x_perm, ws)), W)
+    code = (_ROWS or _rows()).sort(dims, topk_idx, out["counts"], out["offsets"], out["perm"],
+                                   out["inv"], ws, x, x_perm, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_sort")
 
 
 def dispatch(dims, x, inv, x_perm, ws=None, stream=None):
     """moe_dispatch: x_perm[inv[t, j]] = x[t]."""
-    import torch
-    W = "moe_dispatch"
-    T, n, d = dims.T, dims.T * dims.num_experts_per_tok, dims.d_model
-    _check(lib().moe_dispatch(
-        ctypes.byref(dims), _dtype(x, W, "x"), x.data_ptr(), _rows(x, T, d, W, "x"),
-        _flat(inv, n, torch.int32, W, "inv"), x_perm.data_ptr(),
-        _rows(x_perm, n, d, W, "x_perm", x.dtype), _header(ws, W),
-        _launch_on(stream, W, x, inv, x_perm, ws)), W)
+    code = (_ROWS or _rows()).dispatch(dims, x, inv, x_perm, ws, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_dispatch")
 
 
 def dispatch_backward(dims, d_x_perm, inv, d_x, ws=None, add=None, stream=None):
     """moe_dispatch_backward: d_x[t] = sum_j d_x_perm[inv[t, j]] (+ add[t])."""
-    import torch
-    W = "moe_dispatch_backward"
-    T, n, d = dims.T, dims.T * dims.num_experts_per_tok, dims.d_model
-    _check(lib().moe_dispatch_backward(
-        ctypes.byref(dims), _dtype(d_x_perm, W, "d_x_perm"), d_x_perm.data_ptr(),
-        _rows(d_x_perm, n, d, W, "d_x_perm"), _flat(inv, n, torch.int32, W, "inv"), _optional(add),
-        d if add is None else _rows(add, T, d, W, "add", d_x_perm.dtype), _dtype(d_x, W, "d_x"),
-        d_x.data_ptr(), _rows(d_x, T, d, W, "d_x"), _header(ws, W),
-        _launch_on(stream, W, d_x_perm, inv, d_x, ws, add)), W)
+    code = (_ROWS or _rows()).dispatch_backward(dims, d_x_perm, inv, d_x, ws, add, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_dispatch_backward")
 
 
 def combine(dims, o, inv, topk_w, y, ws=None, shared=None, stream=None):
     """moe_combine: y[t] = routed_scaling_factor sum_j topk_w[t, j] o[inv[t, j]] (+ shared[t])."""
-    import torch
-    W = "moe_combine"
-    T, n, d = dims.T, dims.T * dims.num_experts_per_tok, dims.d_model
-    _check(lib().moe_combine(
-        ctypes.byref(dims), _dtype(o, W, "o"), o.data_ptr(), _rows(o, n, d, W, "o"),
-        _flat(inv, n, torch.int32, W, "inv"), _flat(topk_w, n, torch.float32, W, "topk_w"),
-        _optional(shared), d if shared is None else _rows(shared, T, d, W, "shared", o.dtype),
-        _dtype(y, W, "y"), y.data_ptr(), _rows(y, T, d, W, "y"), _header(ws, W),
-        _launch_on(stream, W, o, inv, topk_w, y, ws, shared)), W)
+    code = (_ROWS or _rows()).combine(dims, o, inv, topk_w, y, ws, shared, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_combine")
 
 
 def combine_backward(dims, d_y, o, inv, topk_w, d_o, d_topk_w, ws=None, stream=None):
     """moe_combine_backward: the gradients of combine's o (d_o may be o) and topk_w."""
-    import torch
-    W = "moe_combine_backward"
-    T, n, d = dims.T, dims.T * dims.num_experts_per_tok, dims.d_model
-    _check(lib().moe_combine_backward(
-        ctypes.byref(dims), _dtype(o, W, "o"), d_y.data_ptr(),
-        _rows(d_y, T, d, W, "d_y", o.dtype), o.data_ptr(), _rows(o, n, d, W, "o"),
-        _flat(inv, n, torch.int32, W, "inv"), _flat(topk_w, n, torch.float32, W, "topk_w"),
-        d_o.data_ptr(), _rows(d_o, n, d, W, "d_o", o.dtype),
-        _flat(d_topk_w, n, torch.float32, W, "d_topk_w"), _header(ws, W),
-        _launch_on(stream, W, d_y, o, inv, topk_w, d_o, d_topk_w, ws)), W)
+    code = (_ROWS or _rows()).combine_backward(dims, d_y, o, inv, topk_w, d_o, d_topk_w, ws, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_combine_backward")
 
 
 def route_backward(dims, logits, topk_idx, d_topk_w, d_logits, ws=None, stream=None):
     """moe_route_backward: the gradient of the router's logits [T, E] from that of its weights."""
-    import torch
-    W = "moe_route_backward"
-    T, n, E = dims.T, dims.T * dims.num_experts_per_tok, dims.num_experts
-    f32 = torch.float32
-    _check(lib().moe_route_backward(
-        ctypes.byref(dims), _flat(logits, T * E, f32, W, "logits"),
-        _flat(topk_idx, n, torch.int32, W, "topk_idx"), _flat(d_topk_w, n, f32, W, "d_topk_w"),
-        _flat(d_logits, T * E, f32, W, "d_logits"), _header(ws, W),
-        _launch_on(stream, W, logits, topk_idx, d_topk_w, d_logits, ws)), W)
-
-
-def quantize_int8(x, codes, scales, n_rows=None, stream=None):
-    """moe_quantize_int8: int8 codes and fp32 scales of the rows of x (of its first n_rows[0],
-    a device int32, if given)."""
-    import torch
-    W = "moe_quantize_int8"
-    rows, cols = x.shape
-    _check(lib().moe_quantize_int8(
-        rows, cols, _dtype(x, W, "x"), x.data_ptr(), _rows(x, rows, cols, W, "x"),
-        None if n_rows is None else _flat(n_rows, 1, torch.int32, W, "n_rows"), codes.data_ptr(),
-        _rows(codes, rows, cols, W, "codes", torch.int8),
-        _flat(scales, rows, torch.float32, W, "scales"),
-        _launch_on(stream, W, x, codes, scales, n_rows)), W)
-
-
-def dispatch_int8(dims, x, inv, codes, scales, ws=None, stream=None):
-    """moe_dispatch_int8: each token's row quantized and stored to its slots' expert-order rows."""
-    import torch
-    W = "moe_dispatch_int8"
-    T, n, d = dims.T, dims.T * dims.num_experts_per_tok, dims.d_model
-    _check(lib().moe_dispatch_int8(
-        ctypes.byref(dims), _dtype(x, W, "x"), x.data_ptr(), _rows(x, T, d, W, "x"),
-        _flat(inv, n, torch.int32, W, "inv"), codes.data_ptr(),
-        _rows(codes, n, d, W, "codes", torch.int8), _flat(scales, n, torch.float32, W, "scales"),
-        _header(ws, W), _launch_on(stream, W, x, inv, codes, scales, ws)), W)
+    code = (_ROWS or _rows()).route_backward(dims, logits, topk_idx, d_topk_w, d_logits, ws, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_route_backward")
 
 
 def alloc_codes(rows, cols, device="cuda"):
@@ -569,36 +450,29 @@ def alloc_codes(rows, cols, device="cuda"):
             torch.empty(rows, dtype=torch.float32, device=device))
 
 
+def quantize_int8(x, codes, scales, n_rows=None, stream=None):
+    """moe_quantize_int8: int8 codes and fp32 scales of the rows of x (of its first n_rows[0],
+    a device int32, if given)."""
+    code = (_ROWS or _rows()).quantize_int8(x, codes, scales, n_rows, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_quantize_int8")
+
+
+def dispatch_int8(dims, x, inv, codes, scales, ws=None, stream=None):
+    """moe_dispatch_int8: each token's row quantized and stored to its slots' expert-order rows."""
+    code = (_ROWS or _rows()).dispatch_int8(dims, x, inv, codes, scales, ws, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_dispatch_int8")
+
+
 def matmul_int8(a, a_scale, b, b_scale, out, ws, offsets=None, swiglu=False, stream=None):
     """moe_matmul_int8: out[r, c] = (a[r] . b[g, c]) a_scale[r] b_scale[g, c].
 
     a [M, K] and b [N, K] (or [G, N, K] with offsets [G + 1], the first row of each group) are
     int8; swiglu: b has 2 N rows per group (gate, then up) and out = silu(gate) * up."""
-    import torch
-    W = "moe_matmul_int8"
-    M, K = a.shape
-    grouped = offsets is not None
-    if b.dim() != (3 if grouped else 2) or b.shape[-1] != K:
-        raise _bad(W, f"b: shape {tuple(b.shape)} for a of {tuple(a.shape)}")
-    G, b_rows = (b.shape[0], b.shape[1]) if grouped else (1, b.shape[0])
-    if swiglu and b_rows % 2:
-        raise _bad(W, "b: an odd number of rows for gate and up")
-    N = b_rows // 2 if swiglu else b_rows
-    if grouped and G > 1 and b_rows > 1 and b.stride(0) != b_rows * b.stride(1):
-        raise _bad(W, "b: the groups' rows are not evenly spaced")
-    b2 = b[0] if grouped else b
-    b_stride = _rows(b2, b_rows, K, W, "b", torch.int8)
-    if grouped and b_rows == 1 and G > 1:
-        b_stride = b.stride(0)
-    args = moe_int8_matmul_t(
-        ctypes.sizeof(moe_int8_matmul_t), M, N, K, G, _dtype(out, W, "out"),
-        MOE_INT8_SWIGLU if swiglu else 0, a.data_ptr(), _rows(a, M, K, W, "a", torch.int8),
-        _flat(a_scale, M, torch.float32, W, "a_scale"), b.data_ptr(), b_stride,
-        _flat(b_scale, G * b_rows, torch.float32, W, "b_scale"),
-        _flat(offsets, G + 1, torch.int32, W, "offsets") if grouped else None, out.data_ptr(),
-        _rows(out, M, N, W, "out"))
-    _check(lib().moe_matmul_int8(ctypes.byref(args), ws.data_ptr(), ws.numel(),
-        _launch_on(stream, W, a, a_scale, b, b_scale, out, ws, offsets)), W)
+    code = (_ROWS or _rows()).matmul_int8(a, a_scale, b, b_scale, out, ws, offsets, swiglu, stream)
+    if code != MOE_OK:
+        _raise(code, "moe_matmul_int8")
 
 
 class MoeLayer:

@@ -229,6 +229,35 @@ def test_grouped_matmul(offsets, Mr, dtype, swiglu):
     assert np.all(f64(out)[~inside] == -7) and torch.all(buf[:, N:] == -7)
 
 
+@pytest.mark.parametrize("N,K,pad", [(72, 200, 8), (300, 1300, 0), (257, 1040, 3)])
+@pytest.mark.parametrize("dtype,swiglu", [("bf16", True), ("f16", False), ("f32", False),
+                                          ("f32", True)])
+def test_grouped_matmul_of_large_groups(N, K, pad, dtype, swiglu):
+    """Groups that fill 256-row tiles, between an empty one and a small one; K below and above
+    the depth at which the pipeline's shape changes."""
+    import torch
+    offsets, Mr = [0, 0, 257, 300, 1100, 1111], 1200
+    G, rows_b = len(offsets) - 1, 2 * N if swiglu else N
+    a, da = _matrix(Mr, K, 21)
+    b, db = _matrix(G * rows_b, K, 22)
+    sa, sb = _scales(Mr, 23), _scales(G * rows_b, 24).reshape(G, rows_b)
+    sa = sa * np.float32(4 / np.sqrt(K))
+    out, buf = filled(Mr, N, pad, dtype, -7.0)
+    ws = _header()
+    M.matmul_int8(da, dev(sa), _groups(db, G), dev(sb), out, ws,
+                  offsets=dev(np.array(offsets, dtype=np.int32)), swiglu=swiglu)
+    assert _status(ws) == (0, 0)
+    ref = R.matmul_int8(a, sa, b.reshape(G, rows_b, K), sb, offsets, swiglu)
+    n = offsets[-1]
+    if swiglu:
+        ref, gate, up = ref
+        tol = _swiglu_tol(gate, up, ref, dtype)[:n]
+        assert np.all(np.abs(f64(out) - ref)[:n] <= tol)
+    else:
+        _check(f64(out)[:n], ref[:n], dtype)
+    assert np.all(f64(out)[n:] == -7) and torch.all(buf[:, N:] == -7)
+
+
 def test_swiglu_far_from_zero():
     """Gates from -150 to 150: the activation neither overflows nor turns NaN."""
     import torch

@@ -15,8 +15,17 @@ BAD, SHAPE, SMALL = M.MOE_ERR_INVALID_ARG, M.MOE_ERR_UNSUPPORTED_SHAPE, M.MOE_ER
 
 @pytest.fixture(scope="module")
 def L():
+    """The library with argument types for the calls below (ctypes would pass Python integers
+    as 32-bit ones)."""
     B.build()
-    return M.lib()
+    lib = ctypes.CDLL(M.LIB_PATH)
+    P, I, S, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    kinds = {"D": P, "p": P, "o": P, "q": P, "w": P, "W": P, "s": S, "c": S, "t": I, "z": Z}
+    for name, spec in CALLS.items():
+        getattr(lib, name).argtypes = [kinds[a[0]] for a in spec.split()] + [P]
+    lib.moe_quantize_int8.argtypes = [I, I, I, P, S, P, P, S, P, P]
+    lib.moe_matmul_int8.argtypes = [P, P, Z, P]
+    return lib
 
 
 def _dims(T=64, d=100, E=16, k=4):
@@ -133,7 +142,7 @@ def test_matmul_int8_refusals(L):
     assert L.moe_matmul_int8(None, 4096, 256, None) == BAD
 
 
-def test_binding_refusals_need_no_gpu():
+def test_binding_refusals_need_no_gpu(L):
     import torch
     M_ = M
     dims = _dims(4, 32, 4, 2)
