@@ -338,27 +338,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               continue;
             }
             __syncwarp();
-            const int vec = lane & 3;
-            const int col = chan0 + cb + vec * kVec;
+            const int live = min(32, w.nrows - warp_row);
+            if (p.tma_out && chan0 + cb + kCols <= p.N) {  // 64-byte pieces of 8 rows a store
+              const int vec = lane & 3;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int r = 8 * u + (lane >> 2);
-              if (warp_row + r >= w.nrows) break;
-              const uint4 x =
-                  *reinterpret_cast<const uint4 *>(here + r * 64 + ((vec ^ ((r >> 1) & 3)) << 4));
-              TO *dst = out + static_cast<int64_t>(row0 + r) * p.out_stride + col;
-              if (p.tma_out && col + kVec <= p.N) {
-                *reinterpret_cast<uint4 *>(dst) = x;
-              } else {
-                const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                for (int e = 0; e < kVec; ++e) {
-                  if (col + e >= p.N) break;
-                  if (sizeof(TO) == 4)
-                    reinterpret_cast<uint32_t *>(dst)[e] = y[e % 4];
-                  else
-                    reinterpret_cast<uint16_t *>(dst)[e] =
-                        static_cast<uint16_t>(y[(e / 2) % 4] >> (16 * (e & 1)));
+              for (int u = 0; u < 4; ++u) {
+                const int r = 8 * u + (lane >> 2);
+                if (r >= live) break;
+                *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(row0 + r) * p.out_stride +
+                                           chan0 + cb + vec * kVec) =
+                    *reinterpret_cast<const uint4 *>(here + r * 64 +
+                                                     ((vec ^ ((r >> 1) & 3)) << 4));
+              }
+            } else {  // rows on no 16-byte boundary, or the last channels: a lane per element
+              const int e = lane % kCols;
+              if (chan0 + cb + e < p.N) {
+                for (int r = lane / kCols; r < live; r += 32 / kCols) {
+                  const uint8_t *src = here + r * 64 + (((e / kVec) ^ ((r >> 1) & 3)) << 4) +
+                                       e % kVec * static_cast<int>(sizeof(TO));
+                  out[static_cast<int64_t>(row0 + r) * p.out_stride + chan0 + cb + e] =
+                      *reinterpret_cast<const TO *>(src);
                 }
               }
             }
