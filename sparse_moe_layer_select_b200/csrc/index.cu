@@ -196,7 +196,10 @@ __global__ void __launch_bounds__(512)
                         int with_shared, int *__restrict__ chunk_hist,
                         int32_t *__restrict__ counts, int32_t *__restrict__ offsets,
                         int32_t *__restrict__ perm, int32_t *__restrict__ inv,
-                        Tile *__restrict__ tiles, Tile *__restrict__ tiles_pair, int *header) {
+                        Tile *__restrict__ tiles, Tile *__restrict__ tiles_pair, int *header,
+                        int clear) {
+  // (the histogram's first barrier orders this before anything is recorded)
+  if (clear && threadIdx.x < sizeof(WsHeader) / sizeof(int)) header[threadIdx.x] = 0;
   __shared__ int h[kIdxWarps * kMaxE];
   __shared__ int warp_sums[32];
   __shared__ int totals[3];
@@ -227,15 +230,20 @@ int coop_index_max_ctas() {
 cudaError_t launch_index(const int32_t *topk_idx, int T, int k, int E, int with_shared,
                          int *chunk_hist, Tile *tiles, int *status, int32_t *counts,
                          int32_t *offsets, int32_t *perm, cudaStream_t s, int *launches,
-                         Tile *tiles_pair, int32_t *inv) {
+                         Tile *tiles_pair, int32_t *inv, bool clear) {
   const int n = T * k;
   const int chunk = index_chunk_entries(n);
   const int nchunks = (n + chunk - 1) / chunk;
   if (nchunks == 1) {
     index_single_kernel<<<1, 512, 0, s>>>(topk_idx, n, E, T, with_shared, chunk_hist, counts,
-                                          offsets, perm, inv, tiles, tiles_pair, status);
+                                          offsets, perm, inv, tiles, tiles_pair, status,
+                                          clear ? 1 : 0);
     *launches += 1;
     return cudaGetLastError();
+  }
+  if (clear) {
+    const cudaError_t e = cudaMemsetAsync(status, 0, sizeof(WsHeader), s);
+    if (e != cudaSuccess) return e;
   }
   if (E <= 512 && nchunks <= coop_index_max_ctas()) {
     // one cooperative launch: all chunk CTAs are resident together

@@ -24,6 +24,7 @@
 #include <type_traits>
 
 #include "int8_common.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 
@@ -75,7 +76,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
-  group_tiles(p, kTileRows, first_tile, first_row);
   if (threadIdx.x == 32) {
     for (int s = 0; s < S::stages; ++s) {
       mbar_init(&full[s], 1);
@@ -93,6 +93,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, kTmemCols);
     tmem_relinquish();
   }
+  early_start();
+  group_tiles(p, kTileRows, first_tile, first_row);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -241,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename TO, bool SWIGLU>
 cudaError_t launch_rows(const Int8GemmParams &p, const CUtensorMap &a, const CUtensorMap &b,
                         int grid, cudaStream_t s) {
-  int8_rows_kernel<TO, SWIGLU><<<grid, kThreads, Smem<SWIGLU>::total + 1024, s>>>(p, a, b);
-  return cudaGetLastError();
+  return launch_early(int8_rows_kernel<TO, SWIGLU>, grid, kThreads, Smem<SWIGLU>::total + 1024, s,
+                      p, a, b);
 }
 
 template <typename TO>

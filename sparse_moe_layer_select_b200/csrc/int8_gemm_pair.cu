@@ -25,6 +25,7 @@
 #include <type_traits>
 
 #include "int8_common.cuh"
+#include "pdl.cuh"
 
 namespace moe {
 
@@ -152,6 +153,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
+  early_start();
   group_tiles(p, kTileRows, first_tile, first_row);
   tc_fence_before();
   __syncthreads();
@@ -396,9 +398,8 @@ cudaError_t set_one() {
 template <typename TO, bool SWIGLU>
 cudaError_t launch_one(const Int8GemmParams &p, const CUtensorMap &a, const CUtensorMap &b,
                        const CUtensorMap &out, int grid, cudaStream_t s) {
-  int8_pair_kernel<TO, SWIGLU>
-      <<<grid, kThreads, Smem::bytes(p.ring, p.boxes) + 1024, s>>>(p, a, b, out);
-  return cudaGetLastError();
+  return launch_early(int8_pair_kernel<TO, SWIGLU>, grid, kThreads,
+                      Smem::bytes(p.ring, p.boxes) + 1024, s, p, a, b, out);
 }
 
 }  // namespace

@@ -17,6 +17,7 @@
 #include <type_traits>
 
 #include "kernels.h"
+#include "pdl.cuh"
 #include "rows.cuh"
 #include "status.cuh"
 
@@ -93,6 +94,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
                     const int32_t *__restrict__ n_valid, const int32_t *__restrict__ inv, int k,
                     int d, int chunks, int8_t *__restrict__ codes, int64_t c_stride,
                     float *__restrict__ scales, int *status) {
+  early_start();
   constexpr int kBlock = TPR < 128 ? 128 : TPR;
   constexpr int kWarps = TPR / 32;
   __shared__ uint32_t warp_max[kBlock / 32];
@@ -160,13 +162,10 @@ cudaError_t launch_shape(const void *x, int64_t x_stride, int rows, const int32_
   const int chunks = (d + N - 1) / N;
   const unsigned grid = (rows + kBlock / TPR - 1) / (kBlock / TPR);
   const T *xp = static_cast<const T *>(x);
-  if (inv != nullptr)
-    quantize_kernel<T, N, TPR, R, KEEP, true><<<grid, kBlock, 0, s>>>(
-        xp, x_stride, rows, n_valid, inv, k, d, chunks, codes, c_stride, scales, status);
-  else
-    quantize_kernel<T, N, TPR, R, KEEP, false><<<grid, kBlock, 0, s>>>(
-        xp, x_stride, rows, n_valid, inv, k, d, chunks, codes, c_stride, scales, status);
-  return cudaGetLastError();
+  return launch_early(inv != nullptr ? quantize_kernel<T, N, TPR, R, KEEP, true>
+                                     : quantize_kernel<T, N, TPR, R, KEEP, false>,
+                      grid, kBlock, 0, s, xp, x_stride, rows, n_valid, inv, k, d, chunks, codes,
+                      c_stride, scales, status);
 }
 
 // Threads per row by the row's chunks, so that a thread holds four chunks at most and

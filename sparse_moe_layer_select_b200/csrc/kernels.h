@@ -152,10 +152,11 @@ cudaError_t launch_router_select(float *logits, int nsplit, const uint16_t *x,
                                  cudaStream_t s, const SelectIndexOut *ix = nullptr,
                                  bool *indexed = nullptr);
 
+// clear: the workspace header is zeroed first.
 cudaError_t launch_index(const int32_t *topk_idx, int T, int k, int E, int with_shared,
                          int *chunk_hist, Tile *tiles, int *status, int32_t *counts,
                          int32_t *offsets, int32_t *perm, cudaStream_t s, int *launches,
-                         Tile *tiles_pair = nullptr, int32_t *inv = nullptr);
+                         Tile *tiles_pair = nullptr, int32_t *inv = nullptr, bool clear = false);
 // x_perm[r] = x[perm[r] / k] for r < *n_valid (the routed rows, offsets[E]).
 cudaError_t launch_gather_rows(const uint16_t *x, const int32_t *perm, const int32_t *n_valid,
                                int n_rows, int k, int d, uint16_t *x_perm, cudaStream_t s);

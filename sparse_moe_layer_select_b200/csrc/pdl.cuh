@@ -1,0 +1,39 @@
+// pdl.cuh -- launches that may begin before the kernel ahead of them in the stream has
+// ended (programmatic dependent launch), for runs of short kernels.
+//
+// A kernel launched by launch_early() calls early_start() before it touches global
+// memory: it lets the kernel behind it start, then waits until every kernel ahead of
+// it has completed and its writes are visible.  What a kernel does before that (shared
+// memory barriers, tensor memory, its place in the grid) overlaps the end of the one
+// ahead.  Kernels launched in the ordinary way keep the ordinary order.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <utility>
+
+namespace moe {
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void early_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+#endif
+
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t s, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+
+}  // namespace moe

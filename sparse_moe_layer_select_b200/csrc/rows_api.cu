@@ -97,11 +97,10 @@ moe_status moe_sort(const moe_dims_t *dims, const int32_t *topk_idx, int32_t *co
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char *b = static_cast<char *>(ws);
   int *header = reinterpret_cast<int *>(b);
-  if (cudaMemsetAsync(b, 0, sizeof(WsHeader), s) != cudaSuccess) return MOE_ERR_CUDA;
   int launches = 0;
   if (launch_index(topk_idx, T, k, E, 0, reinterpret_cast<int *>(b + L.hist),
                    reinterpret_cast<Tile *>(b + L.tiles), header, counts, offsets, perm, s,
-                   &launches, nullptr, inv) != cudaSuccess)
+                   &launches, nullptr, inv, true) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (x != nullptr) {
     if (launch_dispatch(dtype, x, x_stride, inv, T, k, d, x_perm, x_perm_stride, header, s) !=

@@ -19,6 +19,7 @@
 // fp32 and rounded once.  An inv entry outside [-1, T k) is skipped and
 // reported, so no row index reaches memory unchecked.
 #include "kernels.h"
+#include "pdl.cuh"
 #include "rows.cuh"
 #include "status.cuh"
 
@@ -86,6 +87,7 @@ __global__ void __launch_bounds__(kThreads)
     dispatch_kernel(const T *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ inv,
                     int n_tokens, int k, int d, int chunks, T *__restrict__ x_perm,
                     int64_t p_stride, int *status) {
+  early_start();
   int t, c;
   if (!item_of(n_tokens, chunks, &t, &c)) return;
   const Chunk<T, N> v = load_chunk<T, N>(x + t * x_stride, c, d);
@@ -110,6 +112,7 @@ __global__ void __launch_bounds__(kThreads)
                      int64_t add_stride, const int32_t *__restrict__ inv,
                      const float *__restrict__ w, int n_tokens, int k, int d, int chunks,
                      float scale, TO *y, int64_t y_stride, int *status) {
+  early_start();
   int t, c;
   if (!item_of(n_tokens, chunks, &t, &c)) return;
   constexpr int B = kBatch<TI, N>;
@@ -158,6 +161,7 @@ __global__ void __launch_bounds__(kThreads)
                             const float *__restrict__ w, int n_slots, int k, int d, int chunks,
                             float scale, T *d_o, int64_t do_stride, float *__restrict__ d_w,
                             int *status) {
+  early_start();
   constexpr int B = kBatch<T, N> / 2;
   const int lane = threadIdx.x & 31;
   const int64_t slot = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
@@ -209,6 +213,7 @@ __global__ void __launch_bounds__(kThreads)
     route_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
                           const float *__restrict__ d_w, int n_tokens, int E, int k, int norm,
                           float *__restrict__ d_logits, int *status) {
+  early_start();
   const int lane = threadIdx.x & 31;
   const int warps = (gridDim.x * kThreads) >> 5;
   for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < n_tokens; t += warps) {
@@ -321,10 +326,8 @@ cudaError_t launch_dispatch(int dtype, const void *x, int64_t x_stride, const in
     return by_chunk(chunk_elems({{x_stride, dtype}, {p_stride, dtype}}), [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      dispatch_kernel<Ty, N><<<all_blocks(static_cast<int64_t>(T) * chunks), kThreads, 0, s>>>(
-          static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
+      return launch_early(dispatch_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * chunks), kThreads, 0, s, static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
           p_stride, status);
-      return cudaGetLastError();
     });
   });
 }
@@ -346,11 +349,8 @@ cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const
         const TI *op = static_cast<const TI *>(o), *ap = static_cast<const TI *>(add);
         TO *yp = static_cast<TO *>(y);
         if (w != nullptr)
-          to_tokens_kernel<TI, TO, N, true><<<grid, kThreads, 0, s>>>(
-              op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
-        else
-          to_tokens_kernel<TI, TO, N, false><<<grid, kThreads, 0, s>>>(
-              op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
+          return launch_early(to_tokens_kernel<TI, TO, N, true>, grid, kThreads, 0, s, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
+        return launch_early(to_tokens_kernel<TI, TO, N, false>, grid, kThreads, 0, s, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
         return cudaGetLastError();
       });
     });
@@ -367,11 +367,8 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride
     return by_chunk(n_elems, [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      combine_backward_kernel<Ty, N>
-          <<<all_blocks(static_cast<int64_t>(T) * k * 32), kThreads, 0, s>>>(
-              static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o), o_stride, inv, w,
+      return launch_early(combine_backward_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * k * 32), kThreads, 0, s, static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o), o_stride, inv, w,
               T * k, k, d, chunks, scale, static_cast<Ty *>(d_o), do_stride, d_w, status);
-      return cudaGetLastError();
     });
   });
 }
@@ -380,13 +377,9 @@ cudaError_t launch_route_backward(const float *logits, const int32_t *topk_idx, 
                                   int T, int E, int k, int norm, float *d_logits, int *status,
                                   cudaStream_t s) {
   const int grid = blocks_for(static_cast<int64_t>(T) * 32);
-  if (E % 4 == 0)
-    route_backward_kernel<4><<<grid, kThreads, 0, s>>>(logits, topk_idx, d_w, T, E, k, norm,
+  return launch_early(E % 4 == 0 ? route_backward_kernel<4> : route_backward_kernel<1>, grid,
+                      kThreads, 0, s, logits, topk_idx, d_w, T, E, k, norm,
                                                        d_logits, status);
-  else
-    route_backward_kernel<1><<<grid, kThreads, 0, s>>>(logits, topk_idx, d_w, T, E, k, norm,
-                                                       d_logits, status);
-  return cudaGetLastError();
 }
 
 }  // namespace moe
