@@ -15,7 +15,7 @@ constexpr int kMaxGroups = 512;
 constexpr int kStageK = 128;  // K elements of a pipeline stage: one 128-byte swizzle row
 
 // One tile of the output: up to the tile's rows of one group by a block of channels.
-struct Work {
+struct alignas(16) Work {
   int group, row0, nrows, ctile;
 };
 
@@ -74,28 +74,45 @@ __device__ __forceinline__ void group_tiles(const Int8GemmParams &p, int tile_ro
   }
 }
 
-// The item's tile.  Items are visited in ascending order: `g` is the group of the last
-// one (0 before the first), and the search goes on from there.
+// The tile of an item, by a search over the groups.
 __device__ __forceinline__ Work find_work(const Int8GemmParams &p, int tile_rows, int item,
-                                          const int *first_tile, const int *first_row, int &g) {
+                                          const int *first_tile, const int *first_row) {
   const int ti = item / p.n_ctiles;
-  if (first_tile[g + 1] <= ti) {
-    int lo = g + 1, hi = p.G - 1;  // the last group whose first tile is <= ti
-    // (a few steps for neighbouring groups, a search for far ones)
-    for (int i = 0; i < 4 && lo < hi && first_tile[lo + 1] <= ti; ++i) ++lo;
-    while (lo < hi && first_tile[lo + 1] <= ti) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (first_tile[mid] <= ti) lo = mid;
-      else hi = mid - 1;
-    }
-    g = lo;
+  int lo = 0, hi = p.G - 1;  // the last group whose first tile is <= ti
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first_tile[mid] <= ti) lo = mid;
+    else hi = mid - 1;
   }
   Work w;
-  w.group = g;
-  w.row0 = first_row[g] + (ti - first_tile[g]) * tile_rows;
-  w.nrows = min(tile_rows, first_row[g + 1] - w.row0);
+  w.group = lo;
+  w.row0 = first_row[lo] + (ti - first_tile[lo]) * tile_rows;
+  w.nrows = min(tile_rows, first_row[lo + 1] - w.row0);
   w.ctile = item - ti * p.n_ctiles;
   return w;
+}
+
+// The tiles of a CTA's items (first, first + step, ...), the first kListed of them found
+// by all threads at once when the kernel starts: a search by the thread that issues the
+// loads, between two items, cost a third of the time of items of 64 KB of weights
+// (256 groups, N = 2048, K = 512, 512 rows: 62 us against 41).
+constexpr int kListed = 256;
+struct ItemList {
+  const Work *list;  // shared
+  const int *first_tile, *first_row;
+  int first, step;
+
+  __device__ __forceinline__ Work operator()(const Int8GemmParams &p, int tile_rows,
+                                             int item) const {
+    const int i = (item - first) / step;
+    return i < kListed ? list[i] : find_work(p, tile_rows, item, first_tile, first_row);
+  }
+};
+__device__ __forceinline__ void list_items(const Int8GemmParams &p, int tile_rows, int first,
+                                           int step, int n_items, const int *first_tile,
+                                           const int *first_row, Work *list) {
+  for (int i = threadIdx.x; i < kListed && first + i * step < n_items; i += blockDim.x)
+    list[i] = find_work(p, tile_rows, first + i * step, first_tile, first_row);
 }
 
 // g sigmoid(g), a few steps of fp32 off; below g = -87, where the exponential is

@@ -9,14 +9,22 @@
 // and the output are rounded once.  Groups are runs of rows: group g owns rows
 // offsets[g] .. offsets[g + 1] - 1 (expert order).
 //
-// int8_rows_kernel: the weights' channels are the M side of the MMA (128 per
-// tile, tcgen05 kind::i8, M = 128) and the rows are its N side, as many columns
-// as the tile has rows (rounded up to 16, at most 128).  With few rows per group
-// every weight byte is brought into shared memory once and the tensor core does
-// no work on empty rows.  One persistent CTA per SM: warp 0 loads by TMA, warp 1
-// issues the MMAs, warps 2-5 drain the accumulators (two, in turn).  The tile
-// list is not stored anywhere: every CTA sums the groups' tile counts from the
-// offsets, and finds an item's group by a search over those sums.
+// int8_rows_kernel (few rows per group; int8_gemm_pair.cu has the other case): the
+// weights' channels are the M side of the MMA (128 per tile, tcgen05 kind::i8,
+// M = 128) and the rows are its N side, as many columns as the tile has rows
+// (rounded up to 16, at most TR).  Every weight byte is brought into shared memory
+// once and the tensor core does no work on empty rows; the weights' bytes bound it.
+// One persistent CTA per SM: warp 0 loads by TMA, warp 1 issues the MMAs, warps 2-5
+// and 6-9 drain the two accumulators, each set every second item: an item of few rows
+// is waiting for memory (its scales), and with one set that took longer than a short
+// item's weights (K = 512: 62 us for 268 MB).  The tile list is not stored anywhere:
+// every CTA sums the groups' tile counts from the offsets and finds its items' groups
+// by a search over those sums, before it starts.
+//
+// One matrix (TR = 32; groups: TR = 128) with fewer tiles than SMs is cut along K as
+// well: a cluster of up to 8 CTAs takes a tile, each a share of K, and sends its
+// integer sums to the CTA that owns their rows (through distributed shared memory;
+// integers, so the order of the sums does not matter).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -32,36 +40,37 @@ namespace {
 
 using namespace int8;
 
-constexpr int kThreads = 192;
+constexpr int kThreads = 320;
 constexpr int kTileChannels = 128;
-constexpr int kTileRows = 128;
-constexpr int kRowBox = 32;                  // rows of one TMA box of a
+constexpr int kRowBox = 32;  // rows of one TMA box of a
 constexpr int kBBytes = kTileChannels * kStageK;
-constexpr int kABytes = kTileRows * kStageK;
-constexpr int kTmemCols = 512;
 
-template <bool SWIGLU>
+template <bool SWIGLU, int TR>
 struct Smem {
-  static constexpr int stages = SWIGLU ? 4 : 6;
-  static constexpr int b_bytes = (SWIGLU ? 2 : 1) * kBBytes;
+  static constexpr int n_acc = SWIGLU ? 2 : 1;  // accumulators of a tile: gate and up
+  static constexpr int stages = TR == 32 ? (SWIGLU ? 5 : 10) : (SWIGLU ? 4 : 6);
+  static constexpr int a_bytes = TR * kStageK;
+  static constexpr int b_bytes = n_acc * kBBytes;
   static constexpr int a_off = stages * b_bytes;
-  static constexpr int bar_off = a_off + stages * kABytes;
-  // full[stages], empty[stages], acc_full[2], acc_empty[2], drain
-  static constexpr int n_bars = 2 * stages + 5;
+  static constexpr int sums_off = a_off + stages * a_bytes;  // sums received (TR = 32 only)
+  static constexpr int bar_off = sums_off + (TR == 32 ? n_acc * TR * kTileChannels * 4 : 0);
+  // full[stages], empty[stages], acc_full[2], acc_empty[2], drain, sums_full
+  static constexpr int n_bars = 2 * stages + 6;
   static constexpr int tmem_slot_off = bar_off + n_bars * 8;
   static constexpr int first_tile_off = tmem_slot_off + 16;  // kMaxGroups + 1 ints
   static constexpr int first_row_off = first_tile_off + (kMaxGroups + 4) * 4;
-  static constexpr int total = first_row_off + (kMaxGroups + 4) * 4;
+  static constexpr int list_off = (first_row_off + (kMaxGroups + 4) * 4 + 15) / 16 * 16;
+  static constexpr int total = list_off + kListed * static_cast<int>(sizeof(Work));
+  static constexpr int tmem_cols = 2 * n_acc * TR;  // two accumulator sets
+  static_assert(total + 1024 <= 232448, "shared memory budget");
 };
-static_assert(Smem<true>::total + 1024 <= 232448 && Smem<false>::total + 1024 <= 232448,
-              "shared memory budget");
 
-template <typename TO, bool SWIGLU>
+template <typename TO, bool SWIGLU, int TR>
 __global__ void __launch_bounds__(kThreads, 1)
     int8_rows_kernel(const __grid_constant__ Int8GemmParams p,
                      const __grid_constant__ CUtensorMap tm_a,
                      const __grid_constant__ CUtensorMap tm_b) {
-  using S = Smem<SWIGLU>;
+  using S = Smem<SWIGLU, TR>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -70,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t *acc_full = empty + S::stages;
   uint64_t *acc_empty = acc_full + 2;
   uint64_t *drain = acc_empty + 2;
+  uint64_t *sums_full = drain + 1;
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + S::tmem_slot_off);
   int *first_tile = reinterpret_cast<int *>(smem + S::first_tile_off);
   int *first_row = reinterpret_cast<int *>(smem + S::first_row_off);
@@ -86,42 +96,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&acc_empty[b], 4);
     }
     mbar_init(drain, 1);
+    mbar_init(sums_full, 4 * p.ksplit);  // the epilogue warps of every CTA of the cluster
     fence_mbar_init();
   }
   if (warp == 1) {
     __syncwarp();
-    tmem_alloc(tmem_slot, kTmemCols);
+    tmem_alloc(tmem_slot, S::tmem_cols);
     tmem_relinquish();
   }
   early_start();
-  group_tiles(p, kTileRows, first_tile, first_row);
+  group_tiles(p, TR, first_tile, first_row);
   tc_fence_before();
   __syncthreads();
+  const int n_items = first_tile[p.G] * p.n_ctiles;
+  const int first = blockIdx.x / p.ksplit;
+  const int step = gridDim.x / p.ksplit;
+  Work *list = reinterpret_cast<Work *>(smem + S::list_off);
+  list_items(p, TR, first, step, n_items, first_tile, first_row, list);
+  const ItemList items{list, first_tile, first_row, first, step};
+  __syncthreads();
+  if (p.ksplit > 1) cluster_sync();  // the others' barriers are ready before any arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int n_items = first_tile[p.G] * p.n_ctiles;
   const int n_kb = (p.K + kStageK - 1) / kStageK;
-  constexpr int kAccStride = SWIGLU ? 256 : 128;  // TMEM columns of one accumulator set
+  constexpr int kAccStride = S::n_acc * TR;  // TMEM columns of one accumulator set
+  // this CTA's share of K (all of it without a cluster), the same items for a whole cluster
+  const int rank = p.ksplit > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(n_kb) * rank / p.ksplit);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(n_kb) * (rank + 1) / p.ksplit);
 
   if (warp == 0) {
     if (lane == 0) {
       int s = 0;
       uint32_t ph = 0;
       long long issued = 0;
-      int group = 0;
       bool ok = true;
-      for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-        const Work w = find_work(p, kTileRows, item, first_tile, first_row, group);
+      for (int item = first; ok && item < n_items; item += step) {
+        const Work w = items(p, TR, item);
         const int boxes = (w.nrows + kRowBox - 1) / kRowBox;
         const int brow = w.group * p.b_rows + (w.ctile * kTileChannels);
-        for (int kb = 0; kb < n_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, p.status, SITE_GEMM_PRODUCER_EMPTY)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&full[s], S::b_bytes + boxes * kRowBox * kStageK);
           uint8_t *b_dst = smem + s * S::b_bytes;
-          uint8_t *a_dst = smem + S::a_off + s * kABytes;
+          uint8_t *a_dst = smem + S::a_off + s * S::a_bytes;
           tma_load_2d(b_dst, &tm_b, &full[s], kb * kStageK, brow);
           if (SWIGLU) tma_load_2d(b_dst + kBBytes, &tm_b, &full[s], kb * kStageK, brow + p.N);
           for (int b = 0; b < boxes; ++b)
@@ -145,29 +166,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
-      int group = 0;
       bool ok = true;
-      for (int item = blockIdx.x; ok && item < n_items; item += gridDim.x) {
-        const Work w = find_work(p, kTileRows, item, first_tile, first_row, group);
+      for (int item = first; ok && item < n_items; item += step) {
+        const Work w = items(p, TR, item);
         const uint32_t idesc = idesc_i8_s32(kTileChannels, (w.nrows + 15) / 16 * 16);
         if (!mbar_wait(&acc_empty[acc], aph ^ 1, p.status, SITE_GEMM_MMA_ACC_EMPTY)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kAccStride;
-        for (int kb = 0; kb < n_kb; ++kb) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait(&full[s], ph, p.status, SITE_GEMM_MMA_FULL)) {
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t b0 = smem_u32(smem + s * S::b_bytes);
-          const uint32_t a0 = smem_u32(smem + S::a_off + s * kABytes);
+          const uint32_t a0 = smem_u32(smem + S::a_off + s * S::a_bytes);
 #pragma unroll
           for (int kk = 0; kk < kStageK / 32; ++kk) {
             umma_i8_ss(d_tmem, smem_desc_sw128(b0 + kk * 32), smem_desc_sw128(a0 + kk * 32), idesc,
-                       (kb | kk) != 0);
+                       kb != kb0 || kk != 0);
             if (SWIGLU)
-              umma_i8_ss(d_tmem + 128, smem_desc_sw128(b0 + kBBytes + kk * 32),
-                         smem_desc_sw128(a0 + kk * 32), idesc, (kb | kk) != 0);
+              umma_i8_ss(d_tmem + TR, smem_desc_sw128(b0 + kBBytes + kk * 32),
+                         smem_desc_sw128(a0 + kk * 32), idesc, kb != kb0 || kk != 0);
           }
           umma_commit(&empty[s]);
           if (++s == S::stages) {
@@ -187,31 +207,93 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;  // this warp's quarter of the accumulator's lanes
-    int acc = 0;
+    const int q = warp & 3;            // this warp's quarter of the accumulator's lanes
+    const int set = (warp - 2) >> 2;   // its accumulator: every second item's
     uint32_t aph = 0;
-    int group = 0;
     float amax = 0.f;
-    for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
-      const Work w = find_work(p, kTileRows, item, first_tile, first_row, group);
+    // (an item's scales are loaded while the set's item before it is worked on)
+    Work next{};
+    float next_sb0 = 0.f, next_sb1 = 0.f, next_sa[TR / 32];
+    auto fetch = [&](int item) {
+      if (item >= n_items) return;
+      next = items(p, TR, item);
+      const int chan = next.ctile * kTileChannels + q * 32 + lane;
+      if (chan < p.N) {
+        const float *sb = p.sb + static_cast<int64_t>(next.group) * p.b_rows + chan;
+        next_sb0 = sb[0];
+        if (SWIGLU) next_sb1 = sb[p.N];
+      }
+#pragma unroll
+      for (int i = 0; i < TR / 32; ++i)
+        next_sa[i] = 32 * i + lane < next.nrows ? p.sa[next.row0 + 32 * i + lane] : 0.f;
+    };
+    fetch(first + set * step);
+    for (int item = first + set * step; item < n_items; item += 2 * step) {
+      const Work w = next;
       const int chan = (w.ctile * kTileChannels) + q * 32 + lane;
       const bool on = chan < p.N;
-      const float *sb = p.sb + static_cast<int64_t>(w.group) * p.b_rows + chan;
-      const float sb0 = on ? sb[0] : 0.f;
-      const float sb1 = SWIGLU && on ? sb[p.N] : 0.f;
-      if (!mbar_wait(&acc_full[acc], aph, p.status, SITE_GEMM_EPI_ACC_FULL)) break;
+      const float sb0 = next_sb0, sb1 = next_sb1;
+      float sa_lane[TR / 32];
+#pragma unroll
+      for (int i = 0; i < TR / 32; ++i) sa_lane[i] = next_sa[i];
+      fetch(item + 2 * step);
+      if (!mbar_wait(&acc_full[set], aph, p.status, SITE_GEMM_EPI_ACC_FULL)) break;
       tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * kAccStride;
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + set * kAccStride;
       TO *out = static_cast<TO *>(p.out) + static_cast<int64_t>(w.row0) * p.out_stride + chan;
-      for (int c = 0; c < w.nrows; c += 16) {
+      if (TR == 32 && p.ksplit > 1) {  // (one item per cluster)
+        // sums_off: [sender][accumulator][row of the owner's][channel]
+        const int per = 32 / p.ksplit;  // rows of the tile that each CTA finishes
+        const uint32_t sums = smem_u32(smem + S::sums_off);
+        const int at = q * 32 + lane;
+#pragma unroll
+        for (int u = 0; u < S::n_acc; ++u) {
+          for (int c = 0; c < w.nrows; c += 16) {
+            uint32_t d[16];
+            tmem_ld_32x32b_x16(taddr + u * TR + c, d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int owner = (c + i) / per;
+              const int slot = (rank * S::n_acc + u) * per + (c + i - owner * per);
+              st_shared_cluster(map_shared_rank(sums + (slot * kTileChannels + at) * 4, owner),
+                                d[i]);
+            }
+          }
+        }
+        fence_cluster();
+        __syncwarp();
+        if (lane < p.ksplit) mbar_arrive_release_cluster(map_shared_rank(smem_u32(sums_full), lane));
+        if (!mbar_wait(sums_full, 0, p.status, SITE_GEMM_EPI_ACC_FULL)) break;
+        fence_cluster();
+        const int *recv = reinterpret_cast<const int *>(smem + S::sums_off) + at;
+        for (int i = 0; i < per && rank * per + i < w.nrows; ++i) {
+          int total[2] = {0, 0};
+          for (int r = 0; r < p.ksplit; ++r)
+#pragma unroll
+            for (int u = 0; u < S::n_acc; ++u)
+              total[u] += recv[((r * S::n_acc + u) * per + i) * kTileChannels];
+          const int row = rank * per + i;
+          const float sa = p.sa[w.row0 + row];
+          float v = static_cast<float>(total[0]) * sa * sb0;
+          if (SWIGLU) v = silu(v) * (static_cast<float>(total[1]) * sa * sb1);
+          if (on) {
+            out[row * p.out_stride] = rows::from_f32<TO>(v);
+            amax = fmaxf(amax, fabsf(v));
+          }
+        }
+        break;
+      }
+#pragma unroll
+      for (int c = 0; c < TR; c += 16) {
+        if (c >= w.nrows) break;
         uint32_t d0[16], d1[16];
         tmem_ld_32x32b_x16(taddr + c, d0);
-        if (SWIGLU) tmem_ld_32x32b_x16(taddr + 128 + c, d1);
-        const float sa_lane = c + (lane & 15) < w.nrows ? p.sa[w.row0 + c + (lane & 15)] : 0.f;
+        if (SWIGLU) tmem_ld_32x32b_x16(taddr + TR + c, d1);
         tmem_ld_wait();
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float sa = __shfl_sync(0xffffffffu, sa_lane, i);
+          const float sa = __shfl_sync(0xffffffffu, sa_lane[c / 32], c % 32 + i);
           float v = static_cast<float>(static_cast<int>(d0[i])) * sa * sb0;
           if (SWIGLU) v = silu(v) * (static_cast<float>(static_cast<int>(d1[i])) * sa * sb1);
           if (on && c + i < w.nrows) {
@@ -222,11 +304,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&acc_empty[acc]);
-      if (++acc == 2) {
-        acc = 0;
-        aph ^= 1;
-      }
+      if (lane == 0) mbar_arrive(&acc_empty[set]);
+      aph ^= 1;
     }
     if (std::is_same<TO, __half>::value && __half2float(__float2half_rn(amax)) == INFINITY)
       record_status(p.status, MOE_ERR_DEVICE_BOUNDS, SITE_H_FP16_RANGE);
@@ -234,28 +313,44 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (p.ksplit > 1) cluster_sync();  // no CTA leaves while another may still write to it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, kTmemCols);
+    tmem_dealloc(tmem_base, S::tmem_cols);
   }
 }
 
-template <typename TO, bool SWIGLU>
+template <typename TO, bool SWIGLU, int TR>
 cudaError_t launch_rows(const Int8GemmParams &p, const CUtensorMap &a, const CUtensorMap &b,
                         int grid, cudaStream_t s) {
-  return launch_early(int8_rows_kernel<TO, SWIGLU>, grid, kThreads, Smem<SWIGLU>::total + 1024, s,
-                      p, a, b);
+  return launch_early(int8_rows_kernel<TO, SWIGLU, TR>, grid, kThreads,
+                      Smem<SWIGLU, TR>::total + 1024, s, p.ksplit, p, a, b);
+}
+
+template <typename TO, bool SWIGLU, int TR>
+cudaError_t set_one() {
+  return cudaFuncSetAttribute(int8_rows_kernel<TO, SWIGLU, TR>,
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              Smem<SWIGLU, TR>::total + 1024);
 }
 
 template <typename TO>
 cudaError_t set_attributes() {
-  cudaError_t e = cudaFuncSetAttribute(int8_rows_kernel<TO, false>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       Smem<false>::total + 1024);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(int8_rows_kernel<TO, true>,
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              Smem<true>::total + 1024);
+  cudaError_t e = set_one<TO, false, 32>();
+  if (e == cudaSuccess) e = set_one<TO, false, 128>();
+  if (e == cudaSuccess) e = set_one<TO, true, 32>();
+  if (e == cudaSuccess) e = set_one<TO, true, 128>();
+  return e;
+}
+
+template <typename TO>
+cudaError_t launch_typed(const Int8GemmParams &p, bool swiglu, int tile_rows, const CUtensorMap &a,
+                         const CUtensorMap &b, int grid, cudaStream_t s) {
+  if (tile_rows == 32)
+    return swiglu ? launch_rows<TO, true, 32>(p, a, b, grid, s)
+                  : launch_rows<TO, false, 32>(p, a, b, grid, s);
+  return swiglu ? launch_rows<TO, true, 128>(p, a, b, grid, s)
+                : launch_rows<TO, false, 128>(p, a, b, grid, s);
 }
 
 }  // namespace
@@ -274,20 +369,25 @@ cudaError_t launch_int8_gemm(Int8GemmParams p, int out_type, bool swiglu, const 
   if (!encode_map_u8(&ma, a, p.M, p.K, a_stride, kRowBox) ||
       !encode_map_u8(&mb, b, static_cast<uint64_t>(p.G) * p.b_rows, p.K, b_stride, kTileChannels))
     return cudaErrorInvalidValue;
+  const int tile_rows = p.offsets == nullptr ? 32 : 128;
   p.n_ctiles = (p.N + kTileChannels - 1) / kTileChannels;
   // at most this many tiles (the device knows the groups' rows)
-  const int64_t tiles = (static_cast<int64_t>(p.M) + kTileRows - 1) / kTileRows + p.G - 1;
-  const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * p.n_ctiles));
+  const int64_t tiles = (static_cast<int64_t>(p.M) + tile_rows - 1) / tile_rows + p.G - 1;
+  p.ksplit = 1;
+  if (p.offsets == nullptr) {
+    // The tiles are known here: K is cut while SMs would be idle, if it is long enough
+    // to pay for the cluster.  1 row, us without / with: N = 1024, K = 2048: 7.5 / 5.9;
+    // N = 4096, K = 8192: 21.9 / 10.3; 64 rows, N = 2048, K = 512 (not cut): 5.9 / 8.9.
+    const int n_kb = (p.K + kStageK - 1) / kStageK;
+    while (n_kb >= 12 && p.ksplit < 8 && tiles * p.n_ctiles * p.ksplit * 2 <= sms &&
+           n_kb >= p.ksplit * 4)
+      p.ksplit *= 2;
+  }
+  const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * p.n_ctiles * p.ksplit));
   switch (out_type) {
-    case MOE_DTYPE_BF16:
-      return swiglu ? launch_rows<__nv_bfloat16, true>(p, ma, mb, grid, s)
-                    : launch_rows<__nv_bfloat16, false>(p, ma, mb, grid, s);
-    case MOE_DTYPE_F16:
-      return swiglu ? launch_rows<__half, true>(p, ma, mb, grid, s)
-                    : launch_rows<__half, false>(p, ma, mb, grid, s);
-    default:
-      return swiglu ? launch_rows<float, true>(p, ma, mb, grid, s)
-                    : launch_rows<float, false>(p, ma, mb, grid, s);
+    case MOE_DTYPE_BF16: return launch_typed<__nv_bfloat16>(p, swiglu, tile_rows, ma, mb, grid, s);
+    case MOE_DTYPE_F16: return launch_typed<__half>(p, swiglu, tile_rows, ma, mb, grid, s);
+    default: return launch_typed<float>(p, swiglu, tile_rows, ma, mb, grid, s);
   }
 }
 

@@ -58,7 +58,9 @@ struct Smem {
   static constexpr int scale_off = bar_off + (n_bars + 1) * 8;  // 64 channel scales per warp
   static constexpr int first_tile_off = scale_off + kEpiWarps * 64 * 4;
   static constexpr int first_row_off = first_tile_off + (kMaxGroups + 4) * 4;
-  static constexpr int ring_off = (first_row_off + (kMaxGroups + 4) * 4 + 1023) / 1024 * 1024;
+  static constexpr int list_off = (first_row_off + (kMaxGroups + 4) * 4 + 15) / 16 * 16;
+  static constexpr int ring_off =
+      (list_off + kListed * static_cast<int>(sizeof(Work)) + 1023) / 1024 * 1024;
   static constexpr int bytes(int ring, int boxes) {
     return ring_off + ring * 2 * kOpBytes + boxes * kEpiWarps * kBoxBytes;
   }
@@ -157,13 +159,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   group_tiles(p, kTileRows, first_tile, first_row);
   tc_fence_before();
   __syncthreads();
+  const int n_items = first_tile[p.G] * p.n_ctiles;
+  const int first = blockIdx.x >> 1;
+  const int step = gridDim.x >> 1;
+  Work *list = reinterpret_cast<Work *>(smem + S::list_off);
+  list_items(p, kTileRows, first, step, n_items, first_tile, first_row, list);
+  const ItemList items{list, first_tile, first_row, first, step};
+  __syncthreads();
   cluster_sync();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  const int n_items = first_tile[p.G] * p.n_ctiles;
   const int n_kb = (p.K + kStageK - 1) / kStageK;
-  const int first = blockIdx.x >> 1;
-  const int step = gridDim.x >> 1;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -171,10 +177,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0;
       uint32_t ph = 0;
       long long issued = 0;
-      int group = 0;
       bool ok = true;
       for (int item = first; ok && item < n_items; item += step) {
-        const Work w = find_work(p, kTileRows, item, first_tile, first_row, group);
+        const Work w = items(p, kTileRows, item);
         const int arow = w.row0 + static_cast<int>(rank) * kHalfRows;
         // SwiGLU: the leader loads the gate channels, its peer the up channels
         const int brow = w.group * p.b_rows + w.ctile * kTileChannels +
@@ -209,7 +214,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = idesc_i8_s32(2 * kHalfRows, 256);
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
-      int group = 0;
       bool ok = true;
       for (int item = first; ok && item < n_items; item += step) {
         if (!mbar_wait(&acc_empty[acc], aph ^ 1, p.status, SITE_GEMM_MMA_ACC_EMPTY)) break;
@@ -259,14 +263,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int warp_row = static_cast<int>(rank) * kHalfRows + q * 32;  // within the tile
     int acc = 0;
     uint32_t aph = 0;
-    int group = 0;
     uint32_t largest = 0;  // of the fp16 outputs, even and odd columns
     // a tile's scales are loaded while the tile before it is worked on
     Work next{};
     float next_sb[2], next_sa = 0.f;
     auto fetch = [&](int item) {
       if (item >= n_items) return;
-      next = find_work(p, kTileRows, item, first_tile, first_row, group);
+      next = items(p, kTileRows, item);
       const float *sb = p.sb + static_cast<int64_t>(next.group) * p.b_rows;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -399,7 +402,7 @@ template <typename TO, bool SWIGLU>
 cudaError_t launch_one(const Int8GemmParams &p, const CUtensorMap &a, const CUtensorMap &b,
                        const CUtensorMap &out, int grid, cudaStream_t s) {
   return launch_early(int8_pair_kernel<TO, SWIGLU>, grid, kThreads,
-                      Smem::bytes(p.ring, p.boxes) + 1024, s, p, a, b, out);
+                      Smem::bytes(p.ring, p.boxes) + 1024, s, 0, p, a, b, out);
 }
 
 }  // namespace

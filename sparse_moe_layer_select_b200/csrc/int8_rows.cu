@@ -164,7 +164,7 @@ cudaError_t launch_shape(const void *x, int64_t x_stride, int rows, const int32_
   const T *xp = static_cast<const T *>(x);
   return launch_early(inv != nullptr ? quantize_kernel<T, N, TPR, R, KEEP, true>
                                      : quantize_kernel<T, N, TPR, R, KEEP, false>,
-                      grid, kBlock, 0, s, xp, x_stride, rows, n_valid, inv, k, d, chunks, codes,
+                      grid, kBlock, 0, s, 0, xp, x_stride, rows, n_valid, inv, k, d, chunks, codes,
                       c_stride, scales, status);
 }
 

@@ -216,6 +216,7 @@ struct Int8GemmParams {
   int n_ctiles;            // channel tiles (set by the launcher)
   int tma_out;             // pair kernel: output rows are a multiple of 16 bytes apart
   int tma_clips;           // and N channels are a multiple of 16 bytes
+  int ksplit;              // rows kernel: CTAs of a cluster, each with a share of K
   int ring, boxes;         // pair kernel: pipeline stages, output boxes per epilogue warp
 };
 // On CTA pairs; clusters: pairs that can be resident at once.

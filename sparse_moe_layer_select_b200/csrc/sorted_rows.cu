@@ -326,7 +326,7 @@ cudaError_t launch_dispatch(int dtype, const void *x, int64_t x_stride, const in
     return by_chunk(chunk_elems({{x_stride, dtype}, {p_stride, dtype}}), [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      return launch_early(dispatch_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * chunks), kThreads, 0, s, static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
+      return launch_early(dispatch_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * chunks), kThreads, 0, s, 0, static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
           p_stride, status);
     });
   });
@@ -349,8 +349,8 @@ cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const
         const TI *op = static_cast<const TI *>(o), *ap = static_cast<const TI *>(add);
         TO *yp = static_cast<TO *>(y);
         if (w != nullptr)
-          return launch_early(to_tokens_kernel<TI, TO, N, true>, grid, kThreads, 0, s, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
-        return launch_early(to_tokens_kernel<TI, TO, N, false>, grid, kThreads, 0, s, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
+          return launch_early(to_tokens_kernel<TI, TO, N, true>, grid, kThreads, 0, s, 0, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
+        return launch_early(to_tokens_kernel<TI, TO, N, false>, grid, kThreads, 0, s, 0, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
         return cudaGetLastError();
       });
     });
@@ -367,7 +367,7 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride
     return by_chunk(n_elems, [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      return launch_early(combine_backward_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * k * 32), kThreads, 0, s, static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o), o_stride, inv, w,
+      return launch_early(combine_backward_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * k * 32), kThreads, 0, s, 0, static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o), o_stride, inv, w,
               T * k, k, d, chunks, scale, static_cast<Ty *>(d_o), do_stride, d_w, status);
     });
   });
@@ -378,7 +378,7 @@ cudaError_t launch_route_backward(const float *logits, const int32_t *topk_idx, 
                                   cudaStream_t s) {
   const int grid = blocks_for(static_cast<int64_t>(T) * 32);
   return launch_early(E % 4 == 0 ? route_backward_kernel<4> : route_backward_kernel<1>, grid,
-                      kThreads, 0, s, logits, topk_idx, d_w, T, E, k, norm,
+                      kThreads, 0, s, 0, logits, topk_idx, d_w, T, E, k, norm,
                                                        d_logits, status);
 }
 
