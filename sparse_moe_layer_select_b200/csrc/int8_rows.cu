@@ -103,7 +103,17 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
   // (threads of one row leave together, and a block of several warps per row has one row)
   if (t >= n_rows || (n_valid != nullptr && t >= *n_valid)) return;
   const T *row = x + t * x_stride;
-  Chunk<T, N> v[R];
+  // the row of lane j's slot: loaded beside the row, given out by shuffles below
+  int dest = kNotRouted;
+  if (DISPATCH && (threadIdx.x & 31) < k) {
+    dest = inv[t * k + (threadIdx.x & 31)];
+    if (dest < 0 || dest >= n_rows * k) {
+      if (dest != kNotRouted && lane < k)
+        record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_INVERSE_ROW);
+      dest = kNotRouted;
+    }
+  }
+  Chunk<T, N> v[R] = {};
   uint32_t m = 0;
   if (KEEP) {
 #pragma unroll
@@ -123,6 +133,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
   }
   float scale, rcp;
   const bool finite = row_scale(m, &scale, &rcp);
+  // (every lane of the warp takes part, also where its chunk is past the row's end)
   auto put = [&](int c, const Chunk<T, N> &val) {
     Codes<N> q = chunk_codes(val, rcp);
     if (!finite) {
@@ -130,27 +141,29 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
       for (int i = 0; i < (N + 3) / 4; ++i) q.w[i] = 0;
     }
     if (!DISPATCH) {
-      store_codes<N>(codes + t * c_stride, c, d, q);
+      if (c < chunks) store_codes<N>(codes + t * c_stride, c, d, q);
     } else {
       for (int j = 0; j < k; ++j) {
-        const int r = inv[t * k + j];
-        if (r >= 0 && r < n_rows * k) store_codes<N>(codes + r * c_stride, c, d, q);
+        const int r = __shfl_sync(0xffffffffu, dest, j);
+        if (c < chunks && r >= 0) store_codes<N>(codes + r * c_stride, c, d, q);
       }
     }
   };
   if (KEEP) {
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (lane + TPR * i < chunks) put(lane + TPR * i, v[i]);
+      if ((lane & ~31) + TPR * i < chunks) put(lane + TPR * i, v[i]);
   } else {
-    for (int c = lane; c < chunks; c += TPR) put(c, load_chunk<T, N>(row, c, d));
+    for (int c = lane; (c & ~31) < chunks; c += TPR) {
+      Chunk<T, N> again{};
+      if (c < chunks) again = load_chunk<T, N>(row, c, d);
+      put(c, again);
+    }
   }
   if (!DISPATCH) {
     if (lane == 0) scales[t] = scale;
-  } else if (lane < k) {
-    const int r = inv[t * k + lane];
-    if (r >= 0 && r < n_rows * k) scales[r] = scale;
-    else if (r != kNotRouted) record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_INVERSE_ROW);
+  } else if (lane < k && dest >= 0) {
+    scales[dest] = scale;
   }
 }
 

@@ -33,7 +33,9 @@ namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 256;
+// (128: at 55 registers a thread, blocks of 256 leave an eighth of the SM's threads unused;
+// combine of 16384 x 4096, top-16: 409 us, with 128 372)
+constexpr int kThreads = 128;
 
 // The expert-order row of a slot, or -1.
 __device__ __forceinline__ int checked_row(int r, int n, int *status) {
@@ -42,20 +44,31 @@ __device__ __forceinline__ int checked_row(int r, int n, int *status) {
   return -1;
 }
 
-// Token and chunk of item i of the T x chunks items (32-bit division where it will do).
+// Chunks of one row that a thread handles, 32 apart: more than one where a chunk is too
+// small to keep enough bytes in flight.
+template <int N>
+constexpr int kPieces = N == 8 ? 1 : 4;
+
+// Token and first chunk of this thread's item: T x chunks items, or for several pieces
+// T x (warps of 32 * pieces chunks).  (32-bit division where it will do.)
+template <int U>
 __device__ __forceinline__ bool item_of(int n_tokens, int chunks, int *t, int *c) {
-  const int64_t total = static_cast<int64_t>(n_tokens) * chunks;
+  const int per_row = U == 1 ? chunks : (chunks + 32 * U - 1) / (32 * U) * 32;
+  const int64_t total = static_cast<int64_t>(n_tokens) * per_row;
   const int64_t i = blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x;
   if (i >= total) return false;
-  if (total <= 0xffffffffLL) *t = static_cast<uint32_t>(i) / static_cast<uint32_t>(chunks);
-  else *t = static_cast<int>(i / chunks);
-  *c = static_cast<int>(i - static_cast<int64_t>(*t) * chunks);
+  if (total <= 0xffffffffLL) *t = static_cast<uint32_t>(i) / static_cast<uint32_t>(per_row);
+  else *t = static_cast<int>(i / per_row);
+  const int at = static_cast<int>(i - static_cast<int64_t>(*t) * per_row);
+  *c = U == 1 ? at : (at & ~31) * U + (at & 31);
   return true;
 }
 
-// Slots whose rows a thread has in flight at once: 128 bytes of loads.
+// Slots whose rows a thread has in flight at once: 128 bytes of loads (twice as many were
+// a fifth slower: fewer threads fit).
 template <typename T, int N>
-constexpr int kBatch = sizeof(T) * N * 16 <= 128 ? 16 : 128 / (sizeof(T) * N);
+constexpr int kBatch = sizeof(T) * N * kPieces<N> * 16 <= 128 ? 16
+                                                              : 128 / (sizeof(T) * N * kPieces<N>);
 
 // Entries [j0, j0 + B) of a token's k slots, four to a load where every token's slots
 // start on a 16-byte boundary; `none` past the last.
@@ -81,16 +94,20 @@ __device__ __forceinline__ void load_slots(const V *slots, int j0, int k, V none
   }
 }
 
-// One thread per (token, chunk): one load, up to k stores.
+// One thread per item: a load per piece, up to k stores of each.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads)
     dispatch_kernel(const T *__restrict__ x, int64_t x_stride, const int32_t *__restrict__ inv,
                     int n_tokens, int k, int d, int chunks, T *__restrict__ x_perm,
                     int64_t p_stride, int *status) {
+  constexpr int U = kPieces<N>;
   early_start();
-  int t, c;
-  if (!item_of(n_tokens, chunks, &t, &c)) return;
-  const Chunk<T, N> v = load_chunk<T, N>(x + t * x_stride, c, d);
+  int t, c0;
+  if (!item_of<U>(n_tokens, chunks, &t, &c0)) return;
+  Chunk<T, N> v[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (U == 1 || c0 + 32 * u < chunks) v[u] = load_chunk<T, N>(x + t * x_stride, c0 + 32 * u, d);
   const int32_t *slots = inv + static_cast<int64_t>(t) * k;
   for (int j0 = 0; j0 < k; j0 += 8) {
     int r[8];
@@ -99,33 +116,43 @@ __global__ void __launch_bounds__(kThreads)
     for (int j = 0; j < 8; ++j) r[j] = checked_row(r[j], n_tokens * k, status);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (r[j] >= 0) store_chunk<T, N>(x_perm + r[j] * p_stride, c, d, v);
+      if (r[j] >= 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (U == 1 || c0 + 32 * u < chunks)
+            store_chunk<T, N>(x_perm + r[j] * p_stride, c0 + 32 * u, d, v[u]);
+      }
   }
 }
 
-// One thread per (token, chunk): up to k loads, kBatch of them in flight, summed in
-// slot order.  y may be add itself: a chunk is read before the same thread
-// overwrites it.
+// One thread per item: up to k loads of each piece, kBatch of them in flight, summed in
+// slot order.  y may be add itself: a chunk is read before the same thread overwrites
+// it.
 template <typename TI, typename TO, int N, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads)
     to_tokens_kernel(const TI *__restrict__ o, int64_t o_stride, const TI *add,
                      int64_t add_stride, const int32_t *__restrict__ inv,
                      const float *__restrict__ w, int n_tokens, int k, int d, int chunks,
                      float scale, TO *y, int64_t y_stride, int *status) {
-  early_start();
-  int t, c;
-  if (!item_of(n_tokens, chunks, &t, &c)) return;
+  constexpr int U = kPieces<N>;
   constexpr int B = kBatch<TI, N>;
+  early_start();
+  int t, c0;
+  if (!item_of<U>(n_tokens, chunks, &t, &c0)) return;
   const int64_t s0 = static_cast<int64_t>(t) * k;
-  Chunk<TI, N> a;
-  if (add != nullptr) a = load_chunk<TI, N>(add + t * add_stride, c, d);
-  float acc[N];
+  Chunk<TI, N> a[U];
+  float acc[U][N];
 #pragma unroll
-  for (int e = 0; e < N; ++e) acc[e] = 0.f;
+  for (int u = 0; u < U; ++u) {
+    if (add != nullptr && (U == 1 || c0 + 32 * u < chunks))
+      a[u] = load_chunk<TI, N>(add + t * add_stride, c0 + 32 * u, d);
+#pragma unroll
+    for (int e = 0; e < N; ++e) acc[u][e] = 0.f;
+  }
   for (int j0 = 0; j0 < k; j0 += B) {
     int r[B];
     float wj[B];
-    Chunk<TI, N> v[B];
+    Chunk<TI, N> v[B][U];
     load_slots(inv + s0, j0, k, kNotRouted, r);
 #pragma unroll
     for (int j = 0; j < B; ++j) {
@@ -135,24 +162,35 @@ __global__ void __launch_bounds__(kThreads)
     if (WEIGHTED) load_slots(w + s0, j0, k, 0.f, wj);
 #pragma unroll
     for (int j = 0; j < B; ++j)
-      if (r[j] >= 0) v[j] = load_chunk<TI, N>(o + r[j] * o_stride, c, d);
+      if (r[j] >= 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (U == 1 || c0 + 32 * u < chunks)
+            v[j][u] = load_chunk<TI, N>(o + r[j] * o_stride, c0 + 32 * u, d);
+      }
 #pragma unroll
     for (int j = 0; j < B; ++j)
       if (r[j] >= 0) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) acc[e] = fmaf(wj[j], element(v[j], e), acc[e]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int e = 0; e < N; ++e) acc[u][e] = fmaf(wj[j], element(v[j][u], e), acc[u][e]);
       }
   }
 #pragma unroll
-  for (int e = 0; e < N; ++e) {
-    if (WEIGHTED) acc[e] *= scale;
-    if (add != nullptr) acc[e] += element(a, e);
+  for (int u = 0; u < U; ++u) {
+    if (U > 1 && c0 + 32 * u >= chunks) break;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      if (WEIGHTED) acc[u][e] *= scale;
+      if (add != nullptr) acc[u][e] += element(a[u], e);
+    }
+    store_chunk<TO, N>(y + t * y_stride, c0 + 32 * u, d, rounded<TO, N>(acc[u]));
   }
-  store_chunk<TO, N>(y + t * y_stride, c, d, rounded<TO, N>(acc));
 }
 
-// One warp per slot: the slot's d_o row and its dot product, kBatch / 2 chunks of
-// both rows in flight.  d_o may be o itself: a chunk is read before the same lane
+// One warp per slot: the slot's d_o row and its dot product, up to 64 bytes of each of
+// the two rows in flight per lane.  d_o may be o itself: a chunk is read before the same lane
 // overwrites it.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads)
@@ -162,7 +200,7 @@ __global__ void __launch_bounds__(kThreads)
                             float scale, T *d_o, int64_t do_stride, float *__restrict__ d_w,
                             int *status) {
   early_start();
-  constexpr int B = kBatch<T, N> / 2;
+  constexpr int B = 64 / (sizeof(T) * N) < 8 ? 64 / (sizeof(T) * N) : 8;
   const int lane = threadIdx.x & 31;
   const int64_t slot = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
   if (slot >= n_slots) return;
@@ -215,8 +253,8 @@ __global__ void __launch_bounds__(kThreads)
                           float *__restrict__ d_logits, int *status) {
   early_start();
   const int lane = threadIdx.x & 31;
-  const int warps = (gridDim.x * kThreads) >> 5;
-  for (int t = (blockIdx.x * kThreads + threadIdx.x) >> 5; t < n_tokens; t += warps) {
+  const int64_t t = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
+  if (t < n_tokens) {
     float *row = d_logits + static_cast<int64_t>(t) * E;
     for (int e = lane * VEC; e < E; e += 32 * VEC) {
       if (VEC == 4) *reinterpret_cast<float4 *>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -263,27 +301,15 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-int sm_count() {
-  static int cached[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  int sms = (dev >= 0 && dev < 64) ? cached[dev] : 0;
-  if (sms == 0) {
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (dev >= 0 && dev < 64) cached[dev] = sms;
-  }
-  return sms;
+// Threads of a kernel that goes by item_of.
+template <int N>
+int64_t items(int T, int chunks) {
+  constexpr int U = kPieces<N>;
+  return static_cast<int64_t>(T) * (U == 1 ? chunks : (chunks + 32 * U - 1) / (32 * U) * 32);
 }
 
 unsigned all_blocks(int64_t threads) {
   return static_cast<unsigned>((threads + kThreads - 1) / kThreads);
-}
-
-// Blocks of kThreads for `work` threads, at most eight per SM (grid-stride loops).
-int blocks_for(int64_t work) {
-  const int64_t want = (work + kThreads - 1) / kThreads;
-  const int64_t cap = static_cast<int64_t>(sm_count()) * 8;
-  return static_cast<int>(want < cap ? (want > 0 ? want : 1) : cap);
 }
 
 // Elements per chunk: 8 where every row starts on a 16-byte boundary, 2 where
@@ -326,7 +352,7 @@ cudaError_t launch_dispatch(int dtype, const void *x, int64_t x_stride, const in
     return by_chunk(chunk_elems({{x_stride, dtype}, {p_stride, dtype}}), [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      return launch_early(dispatch_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * chunks), kThreads, 0, s, 0, static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
+      return launch_early(dispatch_kernel<Ty, N>, all_blocks(items<N>(T, chunks)), kThreads, 0, s, 0, static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
           p_stride, status);
     });
   });
@@ -345,7 +371,7 @@ cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const
         using TO = decltype(to);
         constexpr int N = decltype(n)::value;
         const int chunks = (d + N - 1) / N;
-        const unsigned grid = all_blocks(static_cast<int64_t>(T) * chunks);
+        const unsigned grid = all_blocks(items<N>(T, chunks));
         const TI *op = static_cast<const TI *>(o), *ap = static_cast<const TI *>(add);
         TO *yp = static_cast<TO *>(y);
         if (w != nullptr)
@@ -376,7 +402,7 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride
 cudaError_t launch_route_backward(const float *logits, const int32_t *topk_idx, const float *d_w,
                                   int T, int E, int k, int norm, float *d_logits, int *status,
                                   cudaStream_t s) {
-  const int grid = blocks_for(static_cast<int64_t>(T) * 32);
+  const unsigned grid = all_blocks(static_cast<int64_t>(T) * 32);
   return launch_early(E % 4 == 0 ? route_backward_kernel<4> : route_backward_kernel<1>, grid,
                       kThreads, 0, s, 0, logits, topk_idx, d_w, T, E, k, norm,
                                                        d_logits, status);
