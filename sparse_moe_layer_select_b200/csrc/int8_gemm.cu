@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Work *list = reinterpret_cast<Work *>(smem + S::list_off);
   list_items(p, TR, first, step, n_items, first_tile, first_row, list);
   const ItemList items{list, first_tile, first_row, first, step};
+  const int count = first < n_items ? (n_items - first + step - 1) / step : 0;  // its items
   __syncthreads();
   if (p.ksplit > 1) cluster_sync();  // the others' barriers are ready before any arrival
   tc_fence_after();
@@ -131,8 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       long long issued = 0;
       bool ok = true;
-      for (int item = first; ok && item < n_items; item += step) {
-        const Work w = items(p, TR, item);
+      for (int i = 0; ok && i < count; ++i) {
+        const Work w = items(p, TR, i);
         const int boxes = (w.nrows + kRowBox - 1) / kRowBox;
         const int brow = w.group * p.b_rows + (w.ctile * kTileChannels);
         for (int kb = kb0; kb < kb1; ++kb) {
@@ -167,8 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      for (int item = first; ok && item < n_items; item += step) {
-        const Work w = items(p, TR, item);
+      for (int i = 0; ok && i < count; ++i) {
+        const Work w = items(p, TR, i);
         const uint32_t idesc = idesc_i8_s32(kTileChannels, (w.nrows + 15) / 16 * 16);
         if (!mbar_wait(&acc_empty[acc], aph ^ 1, p.status, SITE_GEMM_MMA_ACC_EMPTY)) break;
         tc_fence_after();
@@ -214,9 +215,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (an item's scales are loaded while the set's item before it is worked on)
     Work next{};
     float next_sb0 = 0.f, next_sb1 = 0.f, next_sa[TR / 32];
-    auto fetch = [&](int item) {
-      if (item >= n_items) return;
-      next = items(p, TR, item);
+    auto fetch = [&](int i) {
+      if (i >= count) return;
+      next = items(p, TR, i);
       const int chan = next.ctile * kTileChannels + q * 32 + lane;
       if (chan < p.N) {
         const float *sb = p.sb + static_cast<int64_t>(next.group) * p.b_rows + chan;
@@ -224,11 +225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (SWIGLU) next_sb1 = sb[p.N];
       }
 #pragma unroll
-      for (int i = 0; i < TR / 32; ++i)
-        next_sa[i] = 32 * i + lane < next.nrows ? p.sa[next.row0 + 32 * i + lane] : 0.f;
+      for (int u = 0; u < TR / 32; ++u)
+        next_sa[u] = 32 * u + lane < next.nrows ? p.sa[next.row0 + 32 * u + lane] : 0.f;
     };
-    fetch(first + set * step);
-    for (int item = first + set * step; item < n_items; item += 2 * step) {
+    fetch(set);
+    for (int it = set; it < count; it += 2) {
       const Work w = next;
       const int chan = (w.ctile * kTileChannels) + q * 32 + lane;
       const bool on = chan < p.N;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sa_lane[TR / 32];
 #pragma unroll
       for (int i = 0; i < TR / 32; ++i) sa_lane[i] = next_sa[i];
-      fetch(item + 2 * step);
+      fetch(it + 2);
       if (!mbar_wait(&acc_full[set], aph, p.status, SITE_GEMM_EPI_ACC_FULL)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + set * kAccStride;
@@ -379,8 +380,11 @@ cudaError_t launch_int8_gemm(Int8GemmParams p, int out_type, bool swiglu, const 
     // to pay for the cluster.  1 row, us without / with: N = 1024, K = 2048: 7.5 / 5.9;
     // N = 4096, K = 8192: 21.9 / 10.3; 64 rows, N = 2048, K = 512 (not cut): 5.9 / 8.9.
     const int n_kb = (p.K + kStageK - 1) / kStageK;
-    while (n_kb >= 12 && p.ksplit < 8 && tiles * p.n_ctiles * p.ksplit * 2 <= sms &&
-           n_kb >= p.ksplit * 4)
+    // (Clusters of 8 for up to 8 tiles only: more of them do not fit on the GPU at once
+    // with a CTA per SM, and 16 took twice as long as 8.)
+    const int64_t all = tiles * p.n_ctiles;
+    while (n_kb >= 12 && n_kb >= p.ksplit * 4 && p.ksplit < (all <= 8 ? 8 : 4) &&
+           all * p.ksplit * 2 <= sms)
       p.ksplit *= 2;
   }
   const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * p.n_ctiles * p.ksplit));

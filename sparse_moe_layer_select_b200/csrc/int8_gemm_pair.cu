@@ -165,6 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   Work *list = reinterpret_cast<Work *>(smem + S::list_off);
   list_items(p, kTileRows, first, step, n_items, first_tile, first_row, list);
   const ItemList items{list, first_tile, first_row, first, step};
+  const int count = first < n_items ? (n_items - first + step - 1) / step : 0;  // its items
   __syncthreads();
   cluster_sync();  // the peer's barriers are initialised before any remote arrival
   tc_fence_after();
@@ -178,8 +179,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t ph = 0;
       long long issued = 0;
       bool ok = true;
-      for (int item = first; ok && item < n_items; item += step) {
-        const Work w = items(p, kTileRows, item);
+      for (int i = 0; ok && i < count; ++i) {
+        const Work w = items(p, kTileRows, i);
         const int arow = w.row0 + static_cast<int>(rank) * kHalfRows;
         // SwiGLU: the leader loads the gate channels, its peer the up channels
         const int brow = w.group * p.b_rows + w.ctile * kTileChannels +
@@ -215,7 +216,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int s = 0, acc = 0;
       uint32_t ph = 0, aph = 0;
       bool ok = true;
-      for (int item = first; ok && item < n_items; item += step) {
+      for (int i = 0; ok && i < count; ++i) {
         if (!mbar_wait(&acc_empty[acc], aph ^ 1, p.status, SITE_GEMM_MMA_ACC_EMPTY)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * kAccStride;
@@ -267,20 +268,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // a tile's scales are loaded while the tile before it is worked on
     Work next{};
     float next_sb[2], next_sa = 0.f;
-    auto fetch = [&](int item) {
-      if (item >= n_items) return;
-      next = items(p, kTileRows, item);
+    auto fetch = [&](int i) {
+      if (i >= count) return;
+      next = items(p, kTileRows, i);
       const float *sb = p.sb + static_cast<int64_t>(next.group) * p.b_rows;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int u = 0; u < 2; ++u) {
         const int chan =
-            next.ctile * kTileChannels + part * kWarpCols + lane + (SWIGLU ? 0 : 32 * i);
-        next_sb[i] = chan < p.N ? sb[(SWIGLU ? i * p.N : 0) + chan] : 0.f;
+            next.ctile * kTileChannels + part * kWarpCols + lane + (SWIGLU ? 0 : 32 * u);
+        next_sb[u] = chan < p.N ? sb[(SWIGLU ? u * p.N : 0) + chan] : 0.f;
       }
       next_sa = warp_row + lane < next.nrows ? p.sa[next.row0 + warp_row + lane] : 0.f;
     };
-    fetch(first);
-    for (int item = first; item < n_items; item += step) {
+    fetch(0);
+    for (int it = 0; it < count; ++it) {
       const Work w = next;
       const float sa = next_sa;
       const int chan0 = w.ctile * kTileChannels + part * kWarpCols;
@@ -290,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int i = 0; i < 2; ++i) sc[i * 32 + lane] = next_sb[i];
       __syncwarp();
-      fetch(item + step);
+      fetch(it + 1);
       if (!mbar_wait(&acc_full[acc], aph, p.status, SITE_GEMM_EPI_ACC_FULL)) break;
       tc_fence_after();
       if (any) {

@@ -280,12 +280,13 @@ moe_status moe_matmul_int8(const moe_int8_matmul_t *m, void *ws, size_t ws_bytes
   p.G = m->G;
   p.b_rows = static_cast<int>(b_rows);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // CTA pairs from 96 rows per group on.  us on 128-row tiles and on pairs, 256 groups:
-  // N = 2048, K = 512: 96 / 102 at 64 rows each, 121 / 98 at 96, 156 / 98 at 128, 444 / 189 at
-  // 512; SwiGLU, N = 512, K = 2048: 115 / 129 at 64, 119 / 131 at 96, 135 / 133 at 128, 307 /
-  // 277 at 512.  One group, N = 2048, K = 4096: 16 / 20 at 16 rows, 22 / 20 at 128, 64 / 33 at
-  // 4096.
-  const bool pairs = m->M >= int64_t(96) * m->G;
+  // CTA pairs where the groups fill their 256-row tiles well enough; the other kernel brings
+  // in the weights once and spends no products on rows that are not there, but a tile of many
+  // rows keeps its epilogue longer than a short K keeps its loads.  us on 128-row tiles and on
+  // pairs, 256 groups: N = 2048, K = 512: 61 / 73 at 32 rows each, 73 / 78 at 48, 87 / 79 at
+  // 64, 101 / 79 at 80; SwiGLU, N = 512, K = 2048: 105 / 127 at 64, 113 / 125 at 96, 131 / 127
+  // at 109.  One group, N = K = 4096: 9.8 / 14.6 at 32 rows, 14.3 / 15.1 at 95.
+  const bool pairs = m->M >= int64_t(m->K <= 1024 ? 56 : 104) * m->G;
   return launched(pairs ? launch_int8_pair(p, m->out_dtype, swiglu, m->a, m->a_stride, m->b,
                                            m->b_stride, clusters, s)
                         : launch_int8_gemm(p, m->out_dtype, swiglu, m->a, m->a_stride, m->b,

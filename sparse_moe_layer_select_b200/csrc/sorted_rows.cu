@@ -241,64 +241,66 @@ __global__ void __launch_bounds__(kThreads)
   if (lane == 0) d_w[i] = scale * dot;
 }
 
-// One warp per token.  The normalised weights are a softmax of log sigmoid(l)
-// over the slots, taken with its maximum out, so that a row whose scores all
-// underflow still has its weights.  The row of d_logits is written whole:
-// zeros, then the selected experts' entries (an expert that a row names twice
-// gets the sum).
+// Half a warp per token (k <= 16).  The normalised weights are a softmax of
+// log sigmoid(l) over the slots, taken with its maximum out, so that a row whose scores
+// all underflow still has its weights.  The row of d_logits is written whole: zeros,
+// then the selected experts' entries (an expert that a row names twice gets the sum).
+// (A warp per token was slower, 14.4 against 10 us for 32768 x 256: each waits for the
+// same two round trips.)
 template <int VEC>
 __global__ void __launch_bounds__(kThreads)
     route_backward_kernel(const float *__restrict__ logits, const int32_t *__restrict__ topk_idx,
                           const float *__restrict__ d_w, int n_tokens, int E, int k, int norm,
                           float *__restrict__ d_logits, int *status) {
   early_start();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 5;
-  if (t < n_tokens) {
-    float *row = d_logits + static_cast<int64_t>(t) * E;
-    for (int e = lane * VEC; e < E; e += 32 * VEC) {
-      if (VEC == 4) *reinterpret_cast<float4 *>(row + e) = make_float4(0.f, 0.f, 0.f, 0.f);
-      else row[e] = 0.f;
+  const int lane = threadIdx.x & 15;
+  const int64_t t = (blockIdx.x * static_cast<int64_t>(kThreads) + threadIdx.x) >> 4;
+  const bool live = t < n_tokens;  // (the other half of the warp may be)
+  float *row = d_logits + t * E;
+  int e = kNotRouted;
+  float g = 0.f;
+  if (live && lane < k) {
+    e = topk_idx[t * k + lane];
+    g = d_w[t * k + lane];
+    if (e < 0 || e >= E) {
+      if (e != kNotRouted) record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_PERMUTE_EXPERT_ID);
+      e = kNotRouted;
     }
-    int e = kNotRouted;
-    if (lane < k) {
-      e = topk_idx[static_cast<int64_t>(t) * k + lane];
-      if (e < 0 || e >= E) {
-        if (e != kNotRouted) record_status(status, MOE_ERR_DEVICE_BOUNDS, SITE_PERMUTE_EXPERT_ID);
-        e = kNotRouted;
-      }
-    }
-    const bool on = e >= 0;
-    const float l = on ? logits[static_cast<int64_t>(t) * E + e] : 0.f;
-    const float g = on ? d_w[static_cast<int64_t>(t) * k + lane] : 0.f;
-    const float q = 1.f / (1.f + expf(l));  // sigmoid(-l)
-    float dl;
-    if (norm) {
-      const float ls = on ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : -INFINITY;
-      float m = ls;
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      float p = on ? expf(ls - m) : 0.f;
-      float sum = p, dot = p * g;
-#pragma unroll
-      for (int off = 8; off > 0; off >>= 1) {
-        sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        dot += __shfl_xor_sync(0xffffffffu, dot, off);
-      }
-      p /= sum;
-      dl = p * q * (g - dot / sum);
-    } else {
-      dl = q / (1.f + expf(-l)) * g;
-    }
-    float total = 0.f;
-    for (int j = 0; j < k; ++j) {
-      const int ej = __shfl_sync(0xffffffffu, e, j);
-      const float dj = __shfl_sync(0xffffffffu, dl, j);
-      if (ej == e) total += dj;
-    }
-    __syncwarp();  // the row's zeros are written
-    if (on) row[e] = total;
   }
+  const bool on = e >= 0;
+  const float l = on ? logits[t * E + e] : 0.f;
+  if (!on) g = 0.f;
+  if (live)
+    for (int c = lane * VEC; c < E; c += 16 * VEC) {
+      if (VEC == 4) *reinterpret_cast<float4 *>(row + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+      else row[c] = 0.f;
+    }
+  const float q = 1.f / (1.f + expf(l));  // sigmoid(-l)
+  float dl;
+  if (norm) {
+    const float ls = on ? fminf(l, 0.f) - log1pf(expf(-fabsf(l))) : -INFINITY;
+    float m = ls;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float p = on ? expf(ls - m) : 0.f;
+    float sum = p, dot = p * g;
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) {
+      sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    }
+    dl = p / sum * q * (g - dot / sum);
+  } else {
+    dl = q / (1.f + expf(-l)) * g;
+  }
+  float total = 0.f;
+  for (int j = 0; j < k; ++j) {
+    const int ej = __shfl_sync(0xffffffffu, e, j, 16);
+    const float dj = __shfl_sync(0xffffffffu, dl, j, 16);
+    if (ej == e) total += dj;
+  }
+  __syncwarp();  // the row's zeros are written
+  if (on) row[e] = total;
 }
 
 // Threads of a kernel that goes by item_of.
@@ -402,7 +404,7 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride
 cudaError_t launch_route_backward(const float *logits, const int32_t *topk_idx, const float *d_w,
                                   int T, int E, int k, int norm, float *d_logits, int *status,
                                   cudaStream_t s) {
-  const unsigned grid = all_blocks(static_cast<int64_t>(T) * 32);
+  const unsigned grid = all_blocks(static_cast<int64_t>(T) * 16);
   return launch_early(E % 4 == 0 ? route_backward_kernel<4> : route_backward_kernel<1>, grid,
                       kThreads, 0, s, 0, logits, topk_idx, d_w, T, E, k, norm,
                                                        d_logits, status);
