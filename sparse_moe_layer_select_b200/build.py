@@ -19,7 +19,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 MOE_SOURCES = ["moe_api.cu", "moe_gemm.cu", "moe_gemm_pair.cu", "moe_fused.cu", "router_cc.cu",
                "index.cu", "elementwise.cu", "permute_static.cu", "sorted_rows.cu", "int8_rows.cu",
-               "int8_gemm.cu", "int8_gemm_pair.cu", "rows_api.cu"]
+               "int8_gemm.cu", "int8_gemm_pair.cu", "int8_gemv.cu", "rows_api.cu"]
 GEN_SOURCES = ["gen.cu"]
 
 

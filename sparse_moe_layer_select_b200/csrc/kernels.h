@@ -227,6 +227,10 @@ cudaError_t launch_int8_gemm(Int8GemmParams p, int out_type, bool swiglu, const 
                              int64_t a_stride, const void *b, int64_t b_stride, int sms,
                              cudaStream_t s);
 
+// For a few rows, on CUDA cores (int8_gemv.cu).
+cudaError_t launch_int8_gemv(const Int8GemmParams &p, int out_type, bool swiglu, const void *a,
+                             int64_t a_stride, const void *b, int64_t b_stride, cudaStream_t s);
+
 // Per-device set-up on the current device (once), its SM count and how many CTA pairs
 // can be resident at once (moe_api.cu).
 cudaError_t current_device_setup(int *sms, int *clusters);

@@ -22,10 +22,10 @@ __device__ __forceinline__ void early_start() {
 
 // cluster: CTAs of a cluster (0: as the kernel is compiled).
 template <typename... P, typename... A>
-cudaError_t launch_early(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem,
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned block, size_t smem,
                          cudaStream_t s, int cluster, A &&...args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

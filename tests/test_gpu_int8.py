@@ -290,6 +290,68 @@ def test_not_a_number_scales_and_the_fp16_range():
     assert _status(ws)[0] == M.MOE_ERR_DEVICE_BOUNDS
 
 
+@pytest.mark.parametrize("Mr,N,K", [(1, 3, 5000), (1, 8192, 4100), (2, 129, 2049), (3, 64, 15),
+                                    (5, 257, 513), (16, 100, 1000), (17, 100, 1000),
+                                    (16, 4096, 1024), (40, 128, 4096), (95, 200, 2048)])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_few_rows(Mr, N, K, swiglu):
+    """The sizes around which the product changes its kernel, with the end of the last row at
+    the end of its allocation."""
+    import torch
+    rows_b = 2 * N if swiglu else N
+    rng = np.random.default_rng(31)
+    a = rng.integers(-127, 128, size=(Mr, K)).astype(np.int8)
+    b = rng.integers(-127, 128, size=(rows_b, K)).astype(np.int8)
+    pitch = (K + 15) // 16 * 16
+    def tight(v):
+        flat = torch.full(((v.shape[0] - 1) * pitch + K,), 99, dtype=torch.int8, device="cuda")
+        t = flat.as_strided(v.shape, (pitch, 1))
+        t.copy_(torch.from_numpy(v))
+        return t
+    sa, sb = _scales(Mr, 32) * np.float32(4 / np.sqrt(K)), _scales(rows_b, 33)
+    out, buf = filled(Mr, N, 5, "f32", -7.0)
+    ws = _header()
+    M.matmul_int8(tight(a), dev(sa), tight(b), dev(sb), out, ws, swiglu=swiglu)
+    assert _status(ws) == (0, 0)
+    ref = R.matmul_int8(a, sa, b[None], sb[None], None, swiglu)
+    if swiglu:
+        ref, gate, up = ref
+        assert np.all(np.abs(f64(out) - ref) <= _swiglu_tol(gate, up, ref, "f32"))
+    else:
+        _check(f64(out), ref, "f32")
+    assert torch.all(buf[:, N:] == -7)
+
+
+@pytest.mark.parametrize("Mr", [1, 8, 16])
+@pytest.mark.parametrize("offsets", [None, [0, 0, 2, 2, 5, 16], [0, 16, 16, 16, 16, 16],
+                                     [3, 4, 4, 6, 6, 7], [0, 9, 4, 30, 2, -1]], ids=str)
+def test_few_rows_in_groups(Mr, offsets):
+    """One expert's row each, empty groups, rows before and behind the groups, bad offsets."""
+    import torch
+    G, N, K = (300 if offsets is None else len(offsets) - 1), 40, 96
+    if offsets is None:
+        offsets = sorted(np.random.default_rng(34).integers(0, Mr + 1, size=G - 1).tolist())
+        offsets = [0] + offsets + [Mr]
+    a, da = _matrix(Mr, K, 35)
+    b, db = _matrix(G * N, K, 36)
+    out, _ = filled(Mr, N, 0, "f32", -7.0)
+    ws = _header()
+    M.matmul_int8(da, torch.ones(Mr, device="cuda"), _groups(db, G),
+                  torch.ones(G * N, device="cuda"), out, ws,
+                  offsets=dev(np.array(offsets, dtype=np.int32)))
+    bad = any(o < 0 or o > Mr for o in offsets) or offsets != sorted(offsets)
+    assert _status(ws)[0] == (M.MOE_ERR_DEVICE_BOUNDS if bad else M.MOE_OK)
+    got = f64(out)
+    for r in range(Mr):
+        ends = np.clip(np.array(offsets[1:]), 0, Mr)
+        g = next((i for i, e in enumerate(ends) if e > r), None)
+        if r < offsets[0] or g is None:
+            assert np.all(got[r] == -7), r
+        else:
+            ref = b[g * N:(g + 1) * N].astype(np.float64) @ a[r].astype(np.float64)
+            assert np.array_equal(got[r], ref), r
+
+
 @pytest.mark.parametrize("offsets", [[0, 30, 20, 40], [-5, 10, 20, 40], [0, 10, 20, 400],
                                      [40, 30, 20, 10], [0, 2 ** 31 - 1, -2 ** 31, 40]])
 def test_bad_offsets_are_clamped_and_reported(offsets):
