@@ -475,12 +475,50 @@ def matmul_int8(a, a_scale, b, b_scale, out, ws, offsets=None, swiglu=False, str
         _raise(code, "moe_matmul_int8")
 
 
+def prepare_int8(W, stream=None):
+    """int8 copies of the expert weights (a model-load step): gate and up rows of each expert in
+    one matrix, as moe_matmul_int8's SwiGLU form takes them.  Returns a dict of codes and scales:
+    gate_up [E, 2F, d], down [E, d, F] and, with a shared expert, s_gate_up [2Fs, d] and
+    s_down [d, Fs]; "<name>_scale" has one fp32 scale per row."""
+    import torch
+
+    def rows(w):
+        q, s = alloc_codes(w.shape[0], w.shape[1], w.device)
+        quantize_int8(w, q, s, stream=stream)
+        return q, s
+
+    E, F, d = W["w_gate"].shape
+    dev = W["w_gate"].device
+    Q = {"gate_up": torch.empty((E, 2 * F, d), dtype=torch.int8, device=dev),
+         "gate_up_scale": torch.empty((E, 2 * F), dtype=torch.float32, device=dev)}
+    for e in range(E):  # one expert at a time: no second copy of the weights is held
+        for i, name in enumerate(("w_gate", "w_up")):
+            quantize_int8(W[name][e], Q["gate_up"][e, i * F:(i + 1) * F],
+                          Q["gate_up_scale"][e, i * F:(i + 1) * F], stream=stream)
+    q, s = rows(W["w_down"].view(E * d, F))
+    Q["down"], Q["down_scale"] = q.view(E, d, F), s.view(E, d)
+    if W.get("ws_gate") is not None:
+        Fs = W["ws_gate"].shape[0]
+        Q["s_gate_up"] = torch.empty((2 * Fs, d), dtype=torch.int8, device=dev)
+        Q["s_gate_up_scale"] = torch.empty(2 * Fs, dtype=torch.float32, device=dev)
+        for i, name in enumerate(("ws_gate", "ws_up")):
+            quantize_int8(W[name], Q["s_gate_up"][i * Fs:(i + 1) * Fs],
+                          Q["s_gate_up_scale"][i * Fs:(i + 1) * Fs], stream=stream)
+        Q["s_down"], Q["s_down_scale"] = rows(W["ws_down"])
+    return Q
+
+
 class MoeLayer:
-    """A layer instance: device weights, routing buffers and workspace, reused across calls."""
+    """A layer instance: device weights, routing buffers and workspace, reused across calls.
+
+    fp8 and int8 keep 8-bit copies of the expert weights instead (one of the two): fp8 by
+    moe_forward_fp8, int8 by the row and 8-bit integer calls in a row (a token mask is taken)."""
 
     def __init__(self, weights: dict, d_model, num_experts, num_experts_per_tok,
                  moe_intermediate_size, shared_intermediate_size, routed_scaling_factor=2.5,
-                 max_tokens=1, flags=0, device="cuda", prepare=True, fp8=False):
+                 max_tokens=1, flags=0, device="cuda", prepare=True, fp8=False, int8=False):
+        if fp8 and int8:
+            raise ValueError("fp8 or int8 experts, not both")
         self.W = dict(weights)
         self.cfg = dict(d_model=d_model, num_experts=num_experts,
                         num_experts_per_tok=num_experts_per_tok,
@@ -489,7 +527,12 @@ class MoeLayer:
                         routed_scaling_factor=routed_scaling_factor, flags=flags)
         self.device = device
         self.fp8 = None
-        if fp8:  # one-time FP8 copies of the expert weights (model-load step)
+        self.int8 = None
+        if int8:  # one-time int8 copies of the expert weights (model-load step)
+            if workspace_size(self.dims(1)) == 0:
+                raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_workspace_size")
+            self.int8 = prepare_int8(self.W)
+        elif fp8:  # one-time FP8 copies of the expert weights (model-load step)
             self.cfg["flags"] |= MOE_FLAG_FP8_EXPERTS
             self.fp8, (code, site) = prepare_fp8(self.dims(1), self.W)
             if code != MOE_OK:
@@ -515,6 +558,51 @@ class MoeLayer:
         self.ws = alloc_workspace(d, self.device)
         self.routing = alloc_routing(d, self.device)
         self._r_struct = routing_struct(self.routing)
+        if self.int8 is not None:
+            import torch
+            c, n = self.cfg, T * d.num_experts_per_tok
+            new = lambda *s, dtype: torch.empty(s, dtype=dtype, device=self.device)  # noqa: E731
+            self.routing["inv"] = new(T, d.num_experts_per_tok, dtype=torch.int32)
+
+            def buffers(rows, F):
+                # the activation stays in fp32 up to its codes: rounded to fp16 first, codes near
+                # a border would move
+                b = {"h": new(rows, F, dtype=torch.float32),
+                     "o": new(rows, c["d_model"], dtype=torch.float16)}
+                b["xq"], b["xs"] = alloc_codes(rows, c["d_model"], self.device)
+                b["hq"], b["hs"] = alloc_codes(rows, F, self.device)
+                return b
+            self._routed = buffers(n, c["moe_intermediate_size"])
+            self._shared = (buffers(T, c["shared_intermediate_size"])
+                            if c["shared_intermediate_size"] else None)
+
+    def _forward_int8(self, d, x, y, stream, token_mask):
+        T, k, E = d.T, d.num_experts_per_tok, d.num_experts
+        Q, R, n = self.int8, self.routing, T * d.num_experts_per_tok
+        out = {"counts": R["counts"], "offsets": R["offsets"], "perm": R["perm"][:n],
+               "inv": R["inv"][:T]}
+        idx, w = R["topk_idx"].view(-1)[:n].view(T, k), R["topk_w"].view(-1)[:n].view(T, k)
+        route(d, x, self.W["w_router"], self.W.get("router_bias"), idx, w, self.ws, stream,
+              token_mask)
+        sort(d, idx, out, self.ws, stream=stream)
+        b = {name: t[:n] for name, t in self._routed.items()}
+        dispatch_int8(d, x, out["inv"], b["xq"], b["xs"], self.ws, stream)
+        matmul_int8(b["xq"], b["xs"], Q["gate_up"], Q["gate_up_scale"], b["h"], self.ws,
+                    R["offsets"], True, stream)
+        quantize_int8(b["h"], b["hq"], b["hs"], R["offsets"][E:], stream)
+        matmul_int8(b["hq"], b["hs"], Q["down"], Q["down_scale"], b["o"], self.ws, R["offsets"],
+                    False, stream)
+        shared = None
+        if self._shared is not None:
+            s = {name: t[:T] for name, t in self._shared.items()}
+            quantize_int8(x, s["xq"], s["xs"], stream=stream)
+            matmul_int8(s["xq"], s["xs"], Q["s_gate_up"], Q["s_gate_up_scale"], s["h"], self.ws,
+                        None, True, stream)
+            quantize_int8(s["h"], s["hq"], s["hs"], stream=stream)
+            matmul_int8(s["hq"], s["hs"], Q["s_down"], Q["s_down_scale"], s["o"], self.ws,
+                        stream=stream)
+            shared = s["o"]
+        combine(d, b["o"], out["inv"], w, y, self.ws, shared, stream)
 
     def forward(self, x, y=None, stream=None, token_mask=None):
         import torch
@@ -524,7 +612,10 @@ class MoeLayer:
         if y is None:
             y = torch.empty_like(x)
         d = self.dims(T)
-        if self.fp8 is not None:
+        if self.int8 is not None:
+            if T > 0:
+                self._forward_int8(d, x, y, stream, token_mask)
+        elif self.fp8 is not None:
             if token_mask is not None:
                 raise ValueError("the FP8-expert forward takes no token mask")
             forward_fp8(d, self._ws_struct, self._q_struct, x, y, self._r_struct, self.ws, stream)
