@@ -1,6 +1,6 @@
 """Build the in-tree shared libraries (nvcc for sm_100a, the host compiler for the binding).
 
-  libmoe_b200.so    the MoE layer (C ABI of include/moe.h)
+  libmoe_b200.so    the MoE layer (C ABI of include/moe.h and include/moe_rows.h)
   libmoe_gen.so     the seeded input generator (test and benchmark inputs only)
   _rows_binding.so  argument marshalling of the row and 8-bit integer calls (CPython module)
 
@@ -41,7 +41,7 @@ def _build_lib(name, sources, extra=(), force=False, verbose=False):
     out = os.path.join(PKG, name)
     deps = [os.path.join(CSRC, s) for s in sources]
     deps += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    deps.append(os.path.join(ROOT, "include", "moe.h"))
+    deps += [os.path.join(ROOT, "include", h) for h in ("moe.h", "moe_rows.h")]
     if not force and not _newer(out, deps):
         return out
     cmd = [_nvcc(), *ARCH, *FLAGS, "-shared", "-o", out + ".tmp",
@@ -57,7 +57,8 @@ def _build_binding(force=False, verbose=False):
     """The CPython module over the C ABI (it reads torch tensors, so it needs torch's headers)."""
     out = os.path.join(PKG, "_rows_binding.so")
     src = os.path.join(CSRC, "rows_binding.cpp")
-    if not force and not _newer(out, [src, os.path.join(ROOT, "include", "moe.h")]):
+    if not force and not _newer(out, [src, *(os.path.join(ROOT, "include", h)
+                                           for h in ("moe.h", "moe_rows.h"))]):
         return out
     import sysconfig
 

@@ -35,6 +35,7 @@
 // themselves are in index_common.cuh.
 #include "index_common.cuh"
 #include "kernels.h"
+#include "rows_kernels.h"
 #include "status.cuh"
 
 namespace moe {
@@ -227,10 +228,13 @@ int coop_index_max_ctas() {
   return cached[dev] > 0 ? cached[dev] : 0;
 }
 
-cudaError_t launch_index(const int32_t *topk_idx, int T, int k, int E, int with_shared,
-                         int *chunk_hist, Tile *tiles, int *status, int32_t *counts,
-                         int32_t *offsets, int32_t *perm, cudaStream_t s, int *launches,
-                         Tile *tiles_pair, int32_t *inv, bool clear) {
+namespace {
+
+// clear: the workspace header is zeroed first (by the kernel itself where one CTA does
+// everything).
+cudaError_t launch(const int32_t *topk_idx, int T, int k, int E, int with_shared, int *chunk_hist,
+                   Tile *tiles, int *status, int32_t *counts, int32_t *offsets, int32_t *perm,
+                   cudaStream_t s, int *launches, Tile *tiles_pair, int32_t *inv, bool clear) {
   const int n = T * k;
   const int chunk = index_chunk_entries(n);
   const int nchunks = (n + chunk - 1) / chunk;
@@ -270,6 +274,23 @@ cudaError_t launch_index(const int32_t *topk_idx, int T, int k, int E, int with_
                                                           chunk / kIdxWarps);
   *launches += 2;
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_index(const int32_t *topk_idx, int T, int k, int E, int with_shared,
+                         int *chunk_hist, Tile *tiles, int *status, int32_t *counts,
+                         int32_t *offsets, int32_t *perm, cudaStream_t s, int *launches,
+                         Tile *tiles_pair, int32_t *inv) {
+  return launch(topk_idx, T, k, E, with_shared, chunk_hist, tiles, status, counts, offsets, perm, s,
+                launches, tiles_pair, inv, false);
+}
+
+cudaError_t launch_index_cleared(const int32_t *topk_idx, int T, int k, int E, int *chunk_hist,
+                                 Tile *tiles, int *header, int32_t *counts, int32_t *offsets,
+                                 int32_t *perm, int32_t *inv, cudaStream_t s, int *launches) {
+  return launch(topk_idx, T, k, E, 0, chunk_hist, tiles, header, counts, offsets, perm, s, launches,
+                nullptr, inv, true);
 }
 
 }  // namespace moe

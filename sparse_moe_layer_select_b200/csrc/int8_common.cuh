@@ -3,9 +3,10 @@
 #pragma once
 #include <cuda_fp16.h>
 
-#include "kernels.h"
-#include "ptx.cuh"
+#include "../../include/moe_rows.h"
+#include "int8_ptx.cuh"
 #include "rows.cuh"
+#include "rows_kernels.h"
 #include "status.cuh"
 
 namespace moe {

@@ -16,9 +16,10 @@
 #include <initializer_list>
 #include <type_traits>
 
-#include "kernels.h"
+#include "../../include/moe_rows.h"
 #include "pdl.cuh"
 #include "rows.cuh"
+#include "rows_kernels.h"
 #include "status.cuh"
 
 namespace moe {

@@ -10,8 +10,9 @@
 #include <cstring>
 #include <mutex>
 
-#include "../../include/moe.h"
+#include "../../include/moe_rows.h"
 #include "kernels.h"
+#include "rows_kernels.h"
 #include "status.cuh"
 
 namespace moe {

@@ -1,4 +1,4 @@
-// rows_api.cu -- entry points of include/moe.h for training and for 8-bit
+// rows_api.cu -- the entry points of include/moe_rows.h, for training and for 8-bit
 // integer products: expert order with its inverse, rows to experts and back,
 // their gradients, quantized rows and their products.  Argument checks and
 // launches only.
@@ -7,8 +7,8 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "../../include/moe.h"
-#include "kernels.h"
+#include "../../include/moe_rows.h"
+#include "rows_kernels.h"
 #include "status.cuh"
 
 namespace {
@@ -98,9 +98,9 @@ moe_status moe_sort(const moe_dims_t *dims, const int32_t *topk_idx, int32_t *co
   char *b = static_cast<char *>(ws);
   int *header = reinterpret_cast<int *>(b);
   int launches = 0;
-  if (launch_index(topk_idx, T, k, E, 0, reinterpret_cast<int *>(b + L.hist),
-                   reinterpret_cast<Tile *>(b + L.tiles), header, counts, offsets, perm, s,
-                   &launches, nullptr, inv, true) != cudaSuccess)
+  if (launch_index_cleared(topk_idx, T, k, E, reinterpret_cast<int *>(b + L.hist),
+                           reinterpret_cast<Tile *>(b + L.tiles), header, counts, offsets, perm,
+                           inv, s, &launches) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (x != nullptr) {
     if (launch_dispatch(dtype, x, x_stride, inv, T, k, d, x_perm, x_perm_stride, header, s) !=

@@ -1,5 +1,5 @@
 // rows_binding.cpp -- argument marshalling of the row and 8-bit integer calls of
-// include/moe.h (module _rows_binding, used by moe.py).
+// include/moe_rows.h (module _rows_binding, used by moe.py).
 //
 // These calls take few microseconds on the device at decode sizes, less than Python
 // needs to ask five tensors for their shapes, strides and addresses and to convert a
@@ -16,7 +16,7 @@
 #include <stdexcept>
 #include <string>
 
-#include "../../include/moe.h"
+#include "../../include/moe_rows.h"
 
 namespace {
 

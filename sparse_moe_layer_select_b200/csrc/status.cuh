@@ -19,8 +19,6 @@ enum Site : int {
   SITE_GEMM_DRAIN = 14,
   SITE_PERMUTE_EXPERT_ID = 20,
   SITE_INDEX_GRID_BARRIER = 21,  // the one-launch index builder's wait for all chunk histograms
-  SITE_INVERSE_ROW = 22,         // inverse-permutation entry outside [-1, T k)
-  SITE_GROUP_OFFSETS = 23,       // group offsets that decrease or leave [0, rows]
   SITE_H_FP16_RANGE = 30,        // SwiGLU activation beyond the fp16 range
   SITE_SLOT_FP16_RANGE = 31,     // scaled expert contribution beyond the fp16 range
   SITE_WEIGHT_FP16_RANGE = 32,   // down-projection weight beyond the fp16 range

@@ -1,4 +1,4 @@
-"""Python binding of the C ABI in include/moe.h (argument marshalling only).
+"""Python binding of the C ABI in include/moe.h and moe_rows.h (argument marshalling only).
 
 Every step of the layer runs in the CUDA kernels of libmoe_b200.so; this
 module only turns torch tensors into device pointers and checks status
@@ -37,10 +37,12 @@ EXPORTED = ["moe_workspace_size", "moe_route", "moe_permute", "moe_forward",
             "moe_read_device_status", "moe_selftest_bounded_wait", "moe_status_string",
             "moe_last_launch_count", "moe_profile_next_forward", "moe_prepare_down_f16",
             "moe_logits_offset", "moe_permute_static", "moe_route_masked",
-            "moe_forward_masked", "moe_prepare_fp8", "moe_forward_fp8",
-            "moe_sort_workspace_size", "moe_sort", "moe_dispatch", "moe_dispatch_backward",
-            "moe_combine", "moe_combine_backward", "moe_route_backward", "moe_quantize_int8",
-            "moe_dispatch_int8", "moe_matmul_int8"]
+            "moe_forward_masked", "moe_prepare_fp8", "moe_forward_fp8"]
+# Those of include/moe_rows.h.
+ROWS_EXPORTED = ["moe_sort_workspace_size", "moe_sort", "moe_dispatch",
+                 "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+                 "moe_route_backward", "moe_quantize_int8", "moe_dispatch_int8",
+                 "moe_matmul_int8"]
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F16 = 1

@@ -1,6 +1,8 @@
 """Row operators and 8-bit products: host-side argument checks (no GPU needed: these paths
 return before any CUDA call) and the oracle's own checks."""
 import ctypes
+import os
+import re
 
 import numpy as np
 import pytest
@@ -10,6 +12,7 @@ from sparse_moe_layer_select_b200 import build as B
 from sparse_moe_layer_select_b200 import moe as M
 from tests.rows_common import routing
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BAD, SHAPE, SMALL = M.MOE_ERR_INVALID_ARG, M.MOE_ERR_UNSUPPORTED_SHAPE, M.MOE_ERR_WORKSPACE_TOO_SMALL
 
 
@@ -87,6 +90,14 @@ def test_argument_errors_return_before_any_launch(L, name):
         empty = [None if a[0] in "poqwW" else v
                  for a, v in zip(CALLS[name].split(), _args(name, _dims(T=0)))]
         assert f(*empty, None) == M.MOE_OK
+
+
+def test_every_declared_symbol_is_exported(L):
+    with open(os.path.join(ROOT, "include", "moe_rows.h")) as f:
+        src = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
+    declared = sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", src)))
+    assert sorted(M.ROWS_EXPORTED) == declared
+    assert all(hasattr(L, name) for name in declared)
 
 
 def test_sort_workspace(L):
