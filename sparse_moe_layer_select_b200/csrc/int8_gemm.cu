@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_slot, S::tmem_cols);
     tmem_relinquish();
   }
-  early_start();
+  wait_for_kernels_ahead();
   group_tiles(p, TR, first_tile, first_row);
   tc_fence_before();
   __syncthreads();

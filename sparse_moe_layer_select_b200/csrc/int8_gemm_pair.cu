@@ -155,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
-  early_start();
+  wait_for_kernels_ahead();
   group_tiles(p, kTileRows, first_tile, first_row);
   tc_fence_before();
   __syncthreads();

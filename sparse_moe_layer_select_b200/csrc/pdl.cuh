@@ -2,10 +2,14 @@
 // ended (programmatic dependent launch), for runs of short kernels.
 //
 // A kernel launched by launch_early() calls early_start() before it touches global
-// memory: it lets the kernel behind it start, then waits until every kernel ahead of
-// it has completed and its writes are visible.  What a kernel does before that (shared
-// memory barriers, tensor memory, its place in the grid) overlaps the end of the one
-// ahead.  Kernels launched in the ordinary way keep the ordinary order.
+// memory: it waits until every kernel ahead of it has completed and its writes are
+// visible.  What a kernel does before that (shared memory barriers, tensor memory, its
+// place in the grid) overlaps the end of the one ahead.  Where its grid is small, it lets
+// the kernel behind it start at once: for 64 tokens' combine, 2.57 against 2.72 us; blocks
+// that wait beside a large grid or a product on tensor cores (which calls
+// wait_for_kernels_ahead()) only cost it (gradients of 4096 tokens: 80.0 against 78.5 us;
+// the 8-bit experts of 64 tokens: 145.5 against 141).  Kernels launched in the ordinary
+// way keep the ordinary order.
 #pragma once
 #include <cuda_runtime.h>
 
@@ -14,9 +18,14 @@
 namespace moe {
 
 #ifdef __CUDACC__
-__device__ __forceinline__ void early_start() {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+__device__ __forceinline__ void wait_for_kernels_ahead() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void early_start() {
+  constexpr unsigned kSmallGrid = 8 * 148;
+  if (gridDim.x * gridDim.y <= kSmallGrid)
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  wait_for_kernels_ahead();
 }
 #endif
 

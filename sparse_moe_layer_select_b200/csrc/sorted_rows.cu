@@ -48,7 +48,7 @@ __device__ __forceinline__ int checked_row(int r, int n, int *status) {
 // Chunks of one row that a thread handles, 32 apart: more than one where a chunk is too
 // small to keep enough bytes in flight.
 template <int N>
-constexpr int kPieces = N == 8 ? 1 : 4;
+constexpr int kPieces = N == 8 ? 1 : 2;
 
 // Token and first chunk of this thread's item: T x chunks items, or for several pieces
 // T x (warps of 32 * pieces chunks).  (32-bit division where it will do.)
@@ -128,11 +128,12 @@ __global__ void __launch_bounds__(kThreads)
 
 // One thread per item: up to k loads of each piece, kBatch of them in flight, summed in
 // slot order.  y may be add itself: a chunk is read before the same thread overwrites
-// it.  (Eight blocks per SM without weights, 64 registers: 345 -> 335 us for the gradient
-// of the copy, 16384 x 4096, top-16; the weighted sum needs 72, and capped it spills:
-// 372 -> 404.)
+// it.  Bound by HBM: 16384 x 4096, top-16, bf16: 360 us, 6.7 TB/s, the gradient of the
+// copy (no weights) 325 us, 7.0 TB/s.  How many blocks fit on an SM decides that: 64
+// registers (weighted) and 56 (not), at 72 and 64 it was 374 and 331 us, at 56 and 48
+// they spill.
 template <typename TI, typename TO, int N, bool WEIGHTED>
-__global__ void __launch_bounds__(kThreads, WEIGHTED ? 1 : 8)
+__global__ void __launch_bounds__(kThreads, WEIGHTED ? 8 : 9)
     to_tokens_kernel(const TI *__restrict__ o, int64_t o_stride, const TI *add,
                      int64_t add_stride, const int32_t *__restrict__ inv,
                      const float *__restrict__ w, int n_tokens, int k, int d, int chunks,
@@ -143,50 +144,53 @@ __global__ void __launch_bounds__(kThreads, WEIGHTED ? 1 : 8)
   int t, c0;
   if (!item_of<U>(n_tokens, chunks, &t, &c0)) return;
   const int64_t s0 = static_cast<int64_t>(t) * k;
-  Chunk<TI, N> a[U];
   float acc[U][N];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (add != nullptr && (U == 1 || c0 + 32 * u < chunks))
-      a[u] = load_chunk<TI, N>(add + t * add_stride, c0 + 32 * u, d);
+  for (int u = 0; u < U; ++u)
 #pragma unroll
     for (int e = 0; e < N; ++e) acc[u][e] = 0.f;
-  }
   for (int j0 = 0; j0 < k; j0 += B) {
-    int r[B];
-    float wj[B];
     Chunk<TI, N> v[B][U];
-    load_slots(inv + s0, j0, k, kNotRouted, r);
+    unsigned routed = 0;
+    {
+      int r[B];
+      load_slots(inv + s0, j0, k, kNotRouted, r);
 #pragma unroll
-    for (int j = 0; j < B; ++j) {
-      r[j] = checked_row(r[j], n_tokens * k, status);
-      wj[j] = 1.f;
+      for (int j = 0; j < B; ++j) {
+        r[j] = checked_row(r[j], n_tokens * k, status);
+        if (r[j] >= 0) routed |= 1u << j;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (r[j] >= 0 && (U == 1 || c0 + 32 * u < chunks))
+            v[j][u] = load_chunk<TI, N>(o + r[j] * o_stride, c0 + 32 * u, d);
+          else
+            v[j][u] = Chunk<TI, N>{};
+        }
+      }
     }
+    float wj[B];
     if (WEIGHTED) load_slots(w + s0, j0, k, 0.f, wj);
 #pragma unroll
-    for (int j = 0; j < B; ++j)
-      if (r[j] >= 0) {
+    for (int j = 0; j < B; ++j) {
+      // a slot that is not routed adds 0 times 0, whatever its weight holds
+      const float f = !WEIGHTED ? 1.f : (routed >> j & 1) ? wj[j] : 0.f;
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-          if (U == 1 || c0 + 32 * u < chunks)
-            v[j][u] = load_chunk<TI, N>(o + r[j] * o_stride, c0 + 32 * u, d);
-      }
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int j = 0; j < B; ++j)
-      if (r[j] >= 0) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-          for (int e = 0; e < N; ++e) acc[u][e] = fmaf(wj[j], element(v[j][u], e), acc[u][e]);
-      }
+        for (int e = 0; e < N; ++e) acc[u][e] = fmaf(f, element(v[j][u], e), acc[u][e]);
+    }
   }
 #pragma unroll
   for (int u = 0; u < U; ++u) {
     if (U > 1 && c0 + 32 * u >= chunks) break;
+    if (WEIGHTED) {
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      if (WEIGHTED) acc[u][e] *= scale;
-      if (add != nullptr) acc[u][e] += element(a[u], e);
+      for (int e = 0; e < N; ++e) acc[u][e] *= scale;
+    }
+    if (add != nullptr) {
+      const Chunk<TI, N> a = load_chunk<TI, N>(add + t * add_stride, c0 + 32 * u, d);
+#pragma unroll
+      for (int e = 0; e < N; ++e) acc[u][e] += element(a, e);
     }
     store_chunk<TO, N>(y + t * y_stride, c0 + 32 * u, d, rounded<TO, N>(acc[u]));
   }
