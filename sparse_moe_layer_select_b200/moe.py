@@ -565,6 +565,9 @@ class MoeLayer:
             c, n = self.cfg, T * d.num_experts_per_tok
             new = lambda *s, dtype: torch.empty(s, dtype=dtype, device=self.device)  # noqa: E731
             self.routing["inv"] = new(T, d.num_experts_per_tok, dtype=torch.int32)
+            # a workspace of its own: moe_sort clears the status word, which the router's call
+            # may have set in self.ws
+            self._sort_ws = alloc_sort_workspace(d, self.device)
 
             def buffers(rows, F):
                 # the activation stays in fp32 up to its codes: rounded to fp16 first, codes near
@@ -586,7 +589,7 @@ class MoeLayer:
         idx, w = R["topk_idx"].view(-1)[:n].view(T, k), R["topk_w"].view(-1)[:n].view(T, k)
         route(d, x, self.W["w_router"], self.W.get("router_bias"), idx, w, self.ws, stream,
               token_mask)
-        sort(d, idx, out, self.ws, stream=stream)
+        sort(d, idx, out, self._sort_ws, stream=stream)
         b = {name: t[:n] for name, t in self._routed.items()}
         dispatch_int8(d, x, out["inv"], b["xq"], b["xs"], self.ws, stream)
         matmul_int8(b["xq"], b["xs"], Q["gate_up"], Q["gate_up_scale"], b["h"], self.ws,
@@ -605,6 +608,13 @@ class MoeLayer:
                         stream=stream)
             shared = s["o"]
         combine(d, b["o"], out["inv"], w, y, self.ws, shared, stream)
+
+    def device_status(self, stream=None):
+        """(code, site) of the first device-side error of the last forward (synchronises)."""
+        status = read_device_status(self.ws, stream)
+        if status[0] == MOE_OK and self.int8 is not None:
+            status = read_device_status(self._sort_ws, stream)
+        return status
 
     def forward(self, x, y=None, stream=None, token_mask=None):
         import torch

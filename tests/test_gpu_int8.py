@@ -373,6 +373,27 @@ def test_bad_offsets_are_clamped_and_reported(offsets):
         assert np.all(got[r] == -7) or any(np.array_equal(got[r], zg[r]) for zg in z)
 
 
+@pytest.mark.parametrize("Mr,offsets,tile", [(17, [0, 9, 17], 128), (64, None, 256)])
+def test_more_items_than_a_block_lists(Mr, offsets, tile):
+    """Some 5 million channels: over 256 tiles for every block, the last ones of which are found
+    by the search alone."""
+    import torch
+    N, K = tile * (148 if tile == 128 else 74) * 262, 16
+    G = 1 if offsets is None else len(offsets) - 1
+    g = torch.Generator(device="cuda").manual_seed(41)
+    a = torch.randint(-127, 128, (Mr, K), generator=g, device="cuda", dtype=torch.int8)
+    b = torch.randint(-127, 128, (G, N, K), generator=g, device="cuda", dtype=torch.int8)
+    out, ws = torch.full((Mr, N), -7.0, device="cuda"), _header()
+    M.matmul_int8(a, torch.ones(Mr, device="cuda"), b if offsets else b[0],
+                  torch.ones(G * N, device="cuda"), out, ws,
+                  offsets=offsets and dev(np.array(offsets, dtype=np.int32)))
+    assert _status(ws) == (0, 0)
+    for i, (lo, hi) in enumerate(zip(offsets or [0], (offsets or [0, Mr])[1:])):
+        for c in range(0, N, 1 << 20):  # sums below 2^24: exact in float32
+            want = a[lo:hi].float() @ b[i, c:c + (1 << 20)].float().t()
+            assert torch.equal(out[lo:hi, c:c + (1 << 20)], want)
+
+
 def test_zero_rows():
     import torch
     e, s = torch.empty(0, 32, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")

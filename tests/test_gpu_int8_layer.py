@@ -62,7 +62,7 @@ def test_layer_with_int8_experts(T, Fs):
     layer = _layer(w, dev)
     y = layer.forward(dev["x"])
     torch.cuda.synchronize()
-    assert M.read_device_status(layer.ws) == (0, 0)
+    assert layer.device_status() == (0, 0)
     idx, wt = (layer.routing[n].cpu().numpy()[:T] for n in ("topk_idx", "topk_w"))
     ref = O.route(h["x"], h["w_router"], None, w.k)
     G.check_routing(idx, wt, {"topk_idx": ref[0], "topk_w": ref[1], "scores": ref[2]}, w.k)

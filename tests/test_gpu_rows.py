@@ -232,6 +232,76 @@ def test_gradients_against_differences():
         assert np.all(np.abs(num - ana) <= 1e-5 * np.abs(f64(d_w)).sum(1) + 1e-12)
 
 
+def test_not_a_number_where_nothing_is_routed():
+    """NaN in the weights, gradients and logits of slots and experts that do not count."""
+    import torch
+    T, d, E, k = 50, 136, 16, 4
+    logits, idx, w = routing(T, E, k, 50, 0.3, True)
+    off = idx < 0
+    inv = R.expert_order(idx, E)[3]
+    dims, ws = _dims(T, d, E, k), M.alloc_sort_workspace(_dims(T, d, E, k))
+    o, dy = rows(T * k, d, 0, "bf16", 51), rows(T, d, 0, "bf16", 52)
+    inv32, bad_w = dev(inv.astype(np.int32)), np.where(off, np.float32("nan"), w)
+    both = []
+    for weight in (w, bad_w):
+        y, d_o = torch.empty_like(dy), torch.zeros_like(o)
+        d_w = torch.empty(T, k, device="cuda")
+        M.combine(dims, o, inv32, dev(weight), y, ws)
+        M.combine_backward(dims, dy, o, inv32, dev(weight), d_o, d_w, ws)
+        both.append((y, d_o, d_w))
+    assert all(torch.equal(a, b) for a, b in zip(*both))
+    g = both[0][2].clone()
+    clean, dirty = torch.empty(T, E, device="cuda"), torch.empty(T, E, device="cuda")
+    M.route_backward(dims, dev(logits), dev(idx), g, clean, ws)
+    chosen = np.zeros((T, E), dtype=bool)
+    t, j = np.nonzero(~off)
+    chosen[t, idx[t, j]] = True
+    g[dev(off)] = float("nan")
+    M.route_backward(dims, dev(np.where(chosen, logits, np.float32("nan"))), dev(idx), g, dirty, ws)
+    assert torch.equal(clean, dirty) and _status(ws) == (0, 0)
+
+
+@pytest.mark.parametrize("dtype,pad", [("bf16", 0), ("f32", 1)])
+def test_sums_in_place_of_their_addend(dtype, pad):
+    import torch
+    T, d, E, k = 77, 200, 16, 4
+    _, idx, w = routing(T, E, k, 60, 0.1)
+    inv = dev(R.expert_order(idx, E)[3].astype(np.int32))
+    dims = _dims(T, d, E, k)
+    o, add = rows(T * k, d, pad, dtype, 61), rows(T, d, pad, dtype, 62)
+    for call in (lambda y, a: M.combine(dims, o, inv, dev(w), y, shared=a),
+                 lambda y, a: M.dispatch_backward(dims, o, inv, y, add=a)):
+        apart = filled(T, d, pad, dtype, 0.0)[0]
+        call(apart, add)
+        same = filled(T, d, pad, dtype, 0.0)[0]
+        same.copy_(add)
+        call(same, same)
+        assert torch.equal(apart, same)
+
+
+def test_calls_on_two_streams_at_once():
+    import torch
+    T, d, E, k = 500, 512, 32, 4
+    _, idx, w = routing(T, E, k, 70, 0.1)
+    dims, di, dw = _dims(T, d, E, k), dev(idx), dev(w)
+    x = rows(T, d, 0, "bf16", 71)
+    work = []
+    for _ in range(2):
+        r, xp = M.alloc_sort(dims), torch.zeros(T * k, d, dtype=torch.bfloat16, device="cuda")
+        work.append((torch.cuda.Stream(), M.alloc_sort_workspace(dims), r, xp, torch.zeros_like(x)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, ws, r, xp, y in work:
+            M.sort(dims, di, r, ws, x=x, x_perm=xp, stream=s)
+            M.combine(dims, xp, r["inv"], dw, y, ws, stream=s)
+    torch.cuda.synchronize()
+    (_, ws, r, xp, y), (_, ws2, r2, xp2, y2) = work
+    assert _status(ws) == (0, 0) and _status(ws2) == (0, 0)
+    n = int(r["offsets"][-1])
+    assert torch.equal(r["inv"], r2["inv"]) and torch.equal(xp[:n], xp2[:n]) and torch.equal(y, y2)
+    assert torch.equal(r["inv"].cpu(), torch.from_numpy(R.expert_order(idx, E)[3].astype(np.int32)))
+
+
 def test_out_of_range_rows_and_experts_are_skipped_and_reported():
     import torch
     T, d, E, k = 6, 32, 4, 2
