@@ -376,16 +376,17 @@ cudaError_t launch_int8_gemm(Int8GemmParams p, int out_type, bool swiglu, const 
   const int64_t tiles = (static_cast<int64_t>(p.M) + tile_rows - 1) / tile_rows + p.G - 1;
   p.ksplit = 1;
   if (p.offsets == nullptr) {
-    // The tiles are known here: K is cut while SMs would be idle, if it is long enough
-    // to pay for the cluster.  1 row, us without / with: N = 1024, K = 2048: 7.5 / 5.9;
-    // N = 4096, K = 8192: 21.9 / 10.3; 64 rows, N = 2048, K = 512 (not cut): 5.9 / 8.9.
+    // The tiles are known here: K is cut while SMs would be idle, if it is long enough to
+    // pay for the cluster.  us without / with: 1 row, N = 1024, K = 2048, 8 ways: 7.5 / 5.9;
+    // 1 row, N = 4096, K = 8192, 4 ways: 21.9 / 10.3; 2 ways: 256 rows, N = 1024, K = 2048:
+    // 9.6 / 11.9, 64 rows, N = 4096, K = 8192: 23.7 / 19.1.  (Clusters of 8 for up to 8
+    // tiles only: more of them do not fit on the GPU at once with a CTA per SM, and 16 took
+    // twice as long as 8.)
     const int n_kb = (p.K + kStageK - 1) / kStageK;
-    // (Clusters of 8 for up to 8 tiles only: more of them do not fit on the GPU at once
-    // with a CTA per SM, and 16 took twice as long as 8.)
     const int64_t all = tiles * p.n_ctiles;
-    while (n_kb >= 12 && n_kb >= p.ksplit * 4 && p.ksplit < (all <= 8 ? 8 : 4) &&
-           all * p.ksplit * 2 <= sms)
-      p.ksplit *= 2;
+    if (all <= 8 && n_kb >= 16) p.ksplit = 8;
+    else if (all * 4 <= sms && n_kb >= 12) p.ksplit = 4;
+    else if (all * 2 <= sms && n_kb >= 48) p.ksplit = 2;
   }
   const int grid = static_cast<int>(std::min<int64_t>(sms, tiles * p.n_ctiles * p.ksplit));
   switch (out_type) {

@@ -293,8 +293,13 @@ moe_status moe_matmul_int8(const moe_int8_matmul_t *m, void *ws, size_t ws_bytes
   // rows keeps its epilogue longer than a short K keeps its loads.  us on 128-row tiles and on
   // pairs, 256 groups: N = 2048, K = 512: 61 / 73 at 32 rows each, 73 / 78 at 48, 87 / 79 at
   // 64, 101 / 79 at 80; SwiGLU, N = 512, K = 2048: 105 / 127 at 64, 113 / 125 at 96, 131 / 127
-  // at 109.  One group, N = K = 4096: 9.8 / 14.6 at 32 rows, 14.3 / 15.1 at 95.
-  const bool pairs = clusters > 0 && m->M >= int64_t(m->K <= 1024 ? 56 : 104) * m->G;
+  // at 109.  One matrix goes to the other kernel's 32-row tiles while they find an SM each:
+  // 512 rows, N = 1024, K = 2048: 9.7 / 11.0; 314 rows, N = 138, K = 1091: 7.9 / 11.7; 95 rows,
+  // N = K = 4096: 14.3 / 15.1.
+  const bool small = m->offsets == nullptr &&
+                     (m->M + 31) / 32 * int64_t((m->N + 127) / 128) <= sms;
+  const bool pairs =
+      clusters > 0 && !small && m->M >= int64_t(m->K <= 1024 ? 56 : 104) * m->G;
   return launched(pairs ? launch_int8_pair(p, m->out_dtype, swiglu, m->a, m->a_stride, m->b,
                                            m->b_stride, clusters, s)
                         : launch_int8_gemm(p, m->out_dtype, swiglu, m->a, m->a_stride, m->b,

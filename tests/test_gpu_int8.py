@@ -292,7 +292,9 @@ def test_not_a_number_scales_and_the_fp16_range():
 
 @pytest.mark.parametrize("Mr,N,K", [(1, 3, 5000), (1, 8192, 4100), (2, 129, 2049), (3, 64, 15),
                                     (5, 257, 513), (16, 100, 1000), (17, 100, 1000),
-                                    (16, 4096, 1024), (40, 128, 4096), (95, 200, 2048)])
+                                    (16, 4096, 1024), (40, 128, 4096), (95, 200, 2048),
+                                    (33, 1200, 1500), (70, 2500, 6200), (300, 900, 600),
+                                    (520, 1100, 300), (600, 1300, 300)])
 @pytest.mark.parametrize("swiglu", [False, True])
 def test_few_rows(Mr, N, K, swiglu):
     """The sizes around which the product changes its kernel, with the end of the last row at
