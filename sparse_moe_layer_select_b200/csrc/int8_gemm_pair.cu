@@ -5,19 +5,22 @@
 // gate and the 128 up channels of the same outputs) with tcgen05.mma.cta_group::2
 // kind::i8, M = 256: each SM holds its own 128 rows of a and half of the channels'
 // rows of b, so every byte brought into shared memory feeds 256 rows or columns.
-// The rows are the accumulator's lanes, so a lane of the epilogue owns a row: it
-// reads 32 columns at a time, the next 32 in flight, scales them by its row's scale and the channels'
-// scales (staged in shared memory per tile) and packs 64 bytes of output; a warp's 32
-// rows of them go out as one TMA box.  (Plain stores, by way of shared memory or not,
-// and TMA boxes of 8 warps were slower: the epilogue is bound by the load/store
-// pipe, and with 8 warps each box waited for the last one's read.)  Boxes that cross
-// the end of a group, and outputs whose rows are no multiple of 16 bytes apart, are
-// stored from shared memory row by row.
+// The rows are the accumulator's lanes, so a lane of the epilogue owns a row: it reads
+// 32 columns at a time, the next 32 in flight, scales them by its row's scale and the
+// channels' scales (staged in shared memory per tile) and packs 64 bytes of output; a
+// warp's 32 rows of them go out as one TMA box.  (Plain stores, by way of shared memory
+// or not, and TMA boxes of 8 warps were slower: the epilogue is bound by the load/store
+// pipe, and with 8 warps each box waited for the last one's read.)  Boxes that cross the
+// end of a group, and outputs whose rows are no multiple of 16 bytes apart, are stored
+// from shared memory row by row.
+//
+// 16384 x 2048 x 4096: 88 us, 3.1e15 operations a second; 262144 rows of 256 experts:
+// gate/up with SwiGLU (N = 512, K = 2048) 485 us, down (N = 2048, K = 512) 350 us.
 //
 // Warps: 0 loads (TMA), 1 MMA issue (leader CTA), 2-17 epilogue, four to a quarter of
-// the lanes, each with a quarter of the columns.  Barriers as in
-// moe_gemm_pair.cu's down GEMM: both CTAs' loads complete on the leader's full[s],
-// commits go to both CTAs.  No TMA or bulk copy uses cluster multicast.
+// the lanes, each with a quarter of the columns.  Barriers as in moe_gemm_pair.cu's
+// down GEMM: both CTAs' loads complete on the leader's full[s], commits go to both CTAs.
+// No TMA or bulk copy uses cluster multicast.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
