@@ -93,7 +93,7 @@ __device__ __forceinline__ Work find_work(const Int8GemmParams &p, int tile_rows
   return w;
 }
 
-// The tiles of a CTA's items (first, first + step, ...; there are `count`), the first kListed of them found
+// The tiles of a CTA's items (first, first + step, ...), the first kListed of them found
 // by all threads at once when the kernel starts: a search by the thread that issues the
 // loads, between two items, cost a third of the time of items of 64 KB of weights
 // (256 groups, N = 2048, K = 512, 512 rows: 62 us against 41).

@@ -29,7 +29,8 @@ __device__ __forceinline__ uint4 load16(const int8_t *row, int k0, int K) {
   uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (k0 + i < K) w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k0 + i])) << (8 * (i % 4));
+    if (k0 + i < K)
+      w[i / 4] |= static_cast<uint32_t>(static_cast<uint8_t>(row[k0 + i])) << (8 * (i % 4));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -59,9 +59,10 @@ template <int N>
 __device__ __forceinline__ void store_codes(int8_t *row, int c, int d, const Codes<N> &q) {
   const int e0 = c * N;
   if (N == 1 || e0 + N <= d) {
-    if constexpr (N == 16) *reinterpret_cast<uint4 *>(row + e0) = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
-    else if constexpr (N == 8) *reinterpret_cast<uint2 *>(row + e0) = make_uint2(q.w[0], q.w[1]);
-    else if constexpr (N == 2) *reinterpret_cast<uint16_t *>(row + e0) = static_cast<uint16_t>(q.w[0]);
+    void *p = row + e0;
+    if constexpr (N == 16) *static_cast<uint4 *>(p) = make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
+    else if constexpr (N == 8) *static_cast<uint2 *>(p) = make_uint2(q.w[0], q.w[1]);
+    else if constexpr (N == 2) *static_cast<uint16_t *>(p) = static_cast<uint16_t>(q.w[0]);
     else row[e0] = static_cast<int8_t>(q.w[0]);
   } else {
 #pragma unroll
@@ -213,8 +214,8 @@ cudaError_t launch_by_chunk(const void *x, int64_t x_stride, int rows, const int
   // rows that all start on a 16-byte boundary move in chunks of 32 bytes (c_stride is a
   // multiple of 16, so their codes are stored 8 or 16 at a time)
   if ((x_stride * static_cast<int64_t>(sizeof(T))) % 16 == 0)
-    return launch_typed<T, 32 / sizeof(T)>(x, x_stride, rows, n_valid, inv, k, d, codes, c_stride, scales,
-                              status, s);
+    return launch_typed<T, 32 / sizeof(T)>(x, x_stride, rows, n_valid, inv, k, d, codes, c_stride,
+                                           scales, status, s);
   if (x_stride % 2 == 0)
     return launch_typed<T, 2>(x, x_stride, rows, n_valid, inv, k, d, codes, c_stride, scales,
                               status, s);

@@ -361,8 +361,9 @@ cudaError_t launch_dispatch(int dtype, const void *x, int64_t x_stride, const in
     return by_chunk(chunk_elems({{x_stride, dtype}, {p_stride, dtype}}), [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      return launch_early(dispatch_kernel<Ty, N>, all_blocks(items<N>(T, chunks)), kThreads, 0, s, 0, static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks, static_cast<Ty *>(x_perm),
-          p_stride, status);
+      return launch_early(dispatch_kernel<Ty, N>, all_blocks(items<N>(T, chunks)), kThreads, 0, s,
+                          0, static_cast<const Ty *>(x), x_stride, inv, T, k, d, chunks,
+                          static_cast<Ty *>(x_perm), p_stride, status);
     });
   });
 }
@@ -383,9 +384,10 @@ cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const
         const unsigned grid = all_blocks(items<N>(T, chunks));
         const TI *op = static_cast<const TI *>(o), *ap = static_cast<const TI *>(add);
         TO *yp = static_cast<TO *>(y);
-        if (w != nullptr)
-          return launch_early(to_tokens_kernel<TI, TO, N, true>, grid, kThreads, 0, s, 0, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
-        return launch_early(to_tokens_kernel<TI, TO, N, false>, grid, kThreads, 0, s, 0, op, o_stride, ap, add_stride, inv, w, T, k, d, chunks, scale, yp, y_stride, status);
+        return launch_early(w != nullptr ? to_tokens_kernel<TI, TO, N, true>
+                                         : to_tokens_kernel<TI, TO, N, false>,
+                            grid, kThreads, 0, s, 0, op, o_stride, ap, add_stride, inv, w, T, k, d,
+                            chunks, scale, yp, y_stride, status);
         return cudaGetLastError();
       });
     });
@@ -402,8 +404,11 @@ cudaError_t launch_combine_backward(int dtype, const void *dy, int64_t dy_stride
     return by_chunk(n_elems, [&](auto n) {
       constexpr int N = decltype(n)::value;
       const int chunks = (d + N - 1) / N;
-      return launch_early(combine_backward_kernel<Ty, N>, all_blocks(static_cast<int64_t>(T) * k * 32), kThreads, 0, s, 0, static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o), o_stride, inv, w,
-              T * k, k, d, chunks, scale, static_cast<Ty *>(d_o), do_stride, d_w, status);
+      return launch_early(combine_backward_kernel<Ty, N>,
+                          all_blocks(static_cast<int64_t>(T) * k * 32), kThreads, 0, s, 0,
+                          static_cast<const Ty *>(dy), dy_stride, static_cast<const Ty *>(o),
+                          o_stride, inv, w, T * k, k, d, chunks, scale, static_cast<Ty *>(d_o),
+                          do_stride, d_w, status);
     });
   });
 }
