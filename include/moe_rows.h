@@ -50,8 +50,9 @@ extern "C" {
  *   reports the first error of the run. */
 typedef enum { MOE_DTYPE_BF16 = 0, MOE_DTYPE_F16 = 1, MOE_DTYPE_F32 = 2 } moe_dtype;
 
-/* Bytes of workspace that moe_sort needs (0 if the dims are invalid); any
- * workspace of moe_workspace_size for the same T, E and k is large enough. */
+/* Bytes of workspace that moe_sort needs for every batch of up to dims->T tokens
+ * (0 if the dims are invalid; never less for more tokens).  For one batch, any
+ * workspace of moe_workspace_size for its T, E and k is large enough. */
 size_t moe_sort_workspace_size(const moe_dims_t *dims);
 
 /* moe_permute with the inverse permutation inv [T, k], and rows of any

@@ -26,11 +26,25 @@ constexpr int kIndexChunk = 4096;   // (token, slot) entries per index-builder c
 // Entries per index-builder chunk for a batch of n (token, slot) entries: one
 // chunk up to kIndexChunk; above that a power of two from 1024 to kIndexChunk,
 // so that mid-sized batches still spread over 32-48 CTAs (one per chunk).
+constexpr int kIndexChunkMin = 1024;
+constexpr int kIndexChunksWanted = 48;
 __host__ __device__ inline int index_chunk_entries(int64_t n) {
   if (n <= kIndexChunk) return kIndexChunk;
-  int c = 1024;
-  while (c < kIndexChunk && static_cast<int64_t>(c) * 48 < n) c *= 2;
+  int c = kIndexChunkMin;
+  while (c < kIndexChunk && static_cast<int64_t>(c) * kIndexChunksWanted < n) c *= 2;
   return c;
+}
+// Chunks of a batch of n entries, and the most that any batch of up to n entries has: the
+// number falls to half wherever the chunk doubles.
+inline int64_t index_chunks(int64_t n) {
+  const int chunk = index_chunk_entries(n);
+  return n > chunk ? (n + chunk - 1) / chunk : 1;
+}
+inline int64_t index_chunks_upto(int64_t n) {
+  const int64_t most = index_chunks(n);
+  return n > static_cast<int64_t>(kIndexChunkMin) * kIndexChunksWanted && most < kIndexChunksWanted
+             ? kIndexChunksWanted
+             : most;
 }
 
 enum GemmMode : int {

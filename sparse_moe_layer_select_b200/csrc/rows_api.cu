@@ -38,17 +38,20 @@ moe_status check_header(const void *ws) {
   return (reinterpret_cast<uintptr_t>(ws) & 255) == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
+int64_t slots(const moe_dims_t *dims) {
+  return static_cast<int64_t>(dims->T) * dims->num_experts_per_tok;
+}
+
 struct SortLayout {
   size_t hist, tiles, total;
 };
 
-SortLayout sort_layout(const moe_dims_t *dims) {
+// The layout of a batch with `nchunks` chunk histograms.
+SortLayout sort_layout(const moe_dims_t *dims, int64_t nchunks) {
   const size_t n = static_cast<size_t>(dims->T) * dims->num_experts_per_tok;
-  const size_t chunk = index_chunk_entries(static_cast<int64_t>(n));
-  const size_t nchunks = std::max<size_t>((n + chunk - 1) / chunk, 1);
   SortLayout L;
   L.hist = a256(sizeof(WsHeader));
-  L.tiles = L.hist + a256(nchunks * dims->num_experts * sizeof(int));
+  L.tiles = L.hist + a256(static_cast<size_t>(nchunks) * dims->num_experts * sizeof(int));
   L.total = L.tiles + a256(((n + kBlockM - 1) / kBlockM + dims->num_experts) * sizeof(Tile));
   return L;
 }
@@ -64,7 +67,9 @@ moe_status launched(cudaError_t e, int launches) {
 extern "C" {
 
 size_t moe_sort_workspace_size(const moe_dims_t *dims) {
-  return check_rows(dims) == MOE_OK ? sort_layout(dims).total : 0;
+  // for every batch of up to T tokens: one just below a step of the chunk size has more chunks
+  if (check_rows(dims) != MOE_OK) return 0;
+  return sort_layout(dims, index_chunks_upto(slots(dims))).total;
 }
 
 moe_status moe_sort(const moe_dims_t *dims, const int32_t *topk_idx, int32_t *counts,
@@ -91,7 +96,7 @@ moe_status moe_sort(const moe_dims_t *dims, const int32_t *topk_idx, int32_t *co
                        x_perm_stride < d))
     return MOE_ERR_INVALID_ARG;
   if (ws == nullptr || (st = check_header(ws)) != MOE_OK) return MOE_ERR_INVALID_ARG;
-  const SortLayout L = sort_layout(dims);
+  const SortLayout L = sort_layout(dims, index_chunks(slots(dims)));
   if (ws_bytes < L.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
   set_last_launch_count(0);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -1,0 +1,45 @@
+"""Limits of the row operators, the 8-bit products and the layers on them: sizes of
+workspaces, refused arguments (no GPU needed: these paths return before any CUDA call)."""
+import pytest
+
+from sparse_moe_layer_select_b200 import build as B
+from sparse_moe_layer_select_b200 import moe as M
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    B.build()
+
+
+# ---------------------------------------------------------------- workspaces
+
+def _chunks(n):
+    """Chunks of the index builder: one up to 4096 entries, above that the smallest of 1024,
+    2048 and 4096 entries that gives at most 48 chunks (4096 if none does)."""
+    if n <= 4096:
+        return 1
+    c = next((c for c in (1024, 2048) if 48 * c >= n), 4096)
+    return -(-n // c)
+
+
+def _sort_bytes(T, E, k):
+    """Bytes that moe_sort uses for one batch: header, chunk histograms, tiles."""
+    r = lambda b: (b + 255) // 256 * 256  # noqa: E731
+    n = T * k
+    return 256 + r(4 * E * _chunks(n)) + r(16 * (-(-n // 128) + E))
+
+
+@pytest.mark.parametrize("E,k", [(1, 1), (16, 4), (256, 8), (512, 3), (512, 16)])
+def test_sort_workspace_serves_every_smaller_batch(E, k):
+    around = {0, 1, 2}
+    for n in (4096, 49152, 98304, 196608):
+        around |= {max(0, n // k + i) for i in (-1, 0, 1, 2)}
+    Ts = sorted(around | set(range(1, 250000 // k, 997)))
+    size = most = 0
+    for T in Ts:
+        n = M.sort_workspace_size(M.make_dims(T, 64, E, k, 0, 0))
+        most = max(most, _sort_bytes(T, E, k))
+        assert n >= size and n >= most, (T, n, size, most)
+        size = n
+    # one batch needs no more than the layer's own workspace for it
+    assert _sort_bytes(5000, 256, 8) <= M.workspace_size(M.make_dims(5000, 64, 256, 8, 64, 0))
