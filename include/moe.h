@@ -167,6 +167,12 @@ typedef struct {
  * dims (0 if the dims are invalid).  The workspace must be 256-byte aligned. */
 size_t moe_workspace_size(const moe_dims_t *dims);
 
+/* The same for every batch of up to dims->T tokens: the largest of their sizes.
+ * (A smaller batch can need more than a larger one: the router keeps a plane of
+ * logits per slice of d, and the index a histogram per chunk, and both numbers fall
+ * in steps as T grows.) */
+size_t moe_workspace_size_upto(const moe_dims_t *dims);
+
 /* Router: sigmoid scores, top-k with ties to the lower expert index, and
  * post-top-k normalisation (Laguna M.1/XS.2 Technical Report summary, Key
  * claims, report §3.1; Laguna-M.1-base spec sheet, Mixture of experts: the

@@ -434,6 +434,25 @@ size_t moe_workspace_size(const moe_dims_t *dims) {
   return ws_layout(D).total;
 }
 
+size_t moe_workspace_size_upto(const moe_dims_t *dims) {
+  Dims D;
+  if (check_dims(dims, &D) != MOE_OK) return 0;
+  size_t most = ws_layout(D).total;
+  // Every section grows with T except where the index's chunks double and where the router
+  // takes fewer K slices: the last batches before those steps are the others to look at.
+  const int64_t steps[] = {
+      int64_t(kIndexChunkMin) * kIndexChunksWanted / D.k,
+      int64_t(2 * kIndexChunkMin) * kIndexChunksWanted / D.k, kRouterSplitSms / 8 * kBlockM,
+      kRouterSplitSms / 4 * kBlockM, kRouterSplitSms / 2 * kBlockM};
+  static_assert(4 * kIndexChunkMin == kIndexChunk, "two steps of the chunk size");
+  for (const int64_t t : steps) {
+    if (t >= dims->T) continue;
+    D.T = static_cast<int>(t);
+    most = std::max(most, ws_layout(D).total);
+  }
+  return most;
+}
+
 moe_status moe_route(const moe_dims_t *dims, const void *x, const void *w_router,
                      const float *router_bias, int32_t *topk_idx, float *topk_w, void *ws,
                      size_t ws_bytes, void *stream) {

@@ -33,7 +33,7 @@ MOE_FLAG_COMBINE_REDUCE = 128
 MOE_FLAG_FUSED_EXPERTS = 256
 
 # Every symbol the header declares (checked by the CPU tests).
-EXPORTED = ["moe_workspace_size", "moe_route", "moe_permute", "moe_forward",
+EXPORTED = ["moe_workspace_size", "moe_workspace_size_upto", "moe_route", "moe_permute", "moe_forward",
             "moe_read_device_status", "moe_selftest_bounded_wait", "moe_status_string",
             "moe_last_launch_count", "moe_profile_next_forward", "moe_prepare_down_f16",
             "moe_logits_offset", "moe_permute_static", "moe_route_masked",
@@ -113,6 +113,8 @@ def lib():
         D = ctypes.POINTER(moe_dims_t)
         L.moe_workspace_size.restype = ctypes.c_size_t
         L.moe_workspace_size.argtypes = [D]
+        L.moe_workspace_size_upto.restype = ctypes.c_size_t
+        L.moe_workspace_size_upto.argtypes = [D]
         L.moe_route.restype = ctypes.c_int
         L.moe_route.argtypes = [D, P, P, P, P, P, P, ctypes.c_size_t, P]
         L.moe_permute.restype = ctypes.c_int
@@ -190,9 +192,15 @@ def workspace_size(dims) -> int:
     return int(lib().moe_workspace_size(ctypes.byref(dims)))
 
 
-def alloc_workspace(dims, device="cuda"):
+def workspace_size_upto(dims) -> int:
+    """The same for every batch of up to dims.T tokens (a smaller batch can need more)."""
+    return int(lib().moe_workspace_size_upto(ctypes.byref(dims)))
+
+
+def alloc_workspace(dims, device="cuda", upto=False):
+    """A workspace for these dims, or (upto) for every batch of up to dims.T tokens."""
     import torch
-    n = workspace_size(dims)
+    n = workspace_size_upto(dims) if upto else workspace_size(dims)
     if n == 0:
         raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_workspace_size")
     return torch.empty(n, dtype=torch.uint8, device=device)
@@ -557,7 +565,7 @@ class MoeLayer:
     def _reserve(self, T):
         self.max_tokens = T
         d = self.dims(T)
-        self.ws = alloc_workspace(d, self.device)
+        self.ws = alloc_workspace(d, self.device, upto=True)
         self.routing = alloc_routing(d, self.device)
         self._r_struct = routing_struct(self.routing)
         if self.int8 is not None:

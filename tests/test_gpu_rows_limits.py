@@ -50,3 +50,20 @@ def test_int8_layer_runs_every_smaller_batch():
         torch.cuda.synchronize()
         assert layers[0].device_status() == layers[1].device_status() == (0, 0)
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,most", [(2304, 2310), (9472, 9473)])
+@pytest.mark.parametrize("int8", [False, True])
+def test_layer_runs_a_batch_with_more_router_planes(T, most, int8):
+    import torch
+    # 2304 and 9472 tokens are the last that the router takes in four and two slices of d
+    w = I.get("c1_tiny").with_(T=most, num_experts=256, num_experts_per_tok=2)
+    h = I.host_inputs(w)
+    ys = []
+    for size in (most, T):
+        layer = M.MoeLayer(G.host_to_device(h), w.d_model, w.E, w.k, w.F, w.Fs,
+                           w.routed_scaling_factor, max_tokens=size, int8=int8)
+        x = G.host_to_device({"x": h["x"][:T]})["x"]
+        ys.append(layer.forward(x))
+        assert layer.device_status() == (0, 0)
+    assert torch.equal(*ys)

@@ -43,3 +43,23 @@ def test_sort_workspace_serves_every_smaller_batch(E, k):
         size = n
     # one batch needs no more than the layer's own workspace for it
     assert _sort_bytes(5000, 256, 8) <= M.workspace_size(M.make_dims(5000, 64, 256, 8, 64, 0))
+
+
+@pytest.mark.parametrize("E,k,d,F,Fs,flags", [
+    (16, 4, 256, 128, 128, 0), (256, 8, 2048, 512, 512, M.MOE_FLAG_DOWN_F16),
+    (256, 1, 64, 64, 0, M.MOE_FLAG_DOWN_F16), (512, 1, 64, 64, 0, M.MOE_FLAG_DOWN_F16),
+    (256, 2, 128, 128, 0, M.MOE_FLAG_FUSED_EXPERTS | M.MOE_FLAG_DOWN_F16),
+    (256, 2, 256, 64, 0, M.MOE_FLAG_ROUTER_TENSOR | M.MOE_FLAG_DOWN_F16),
+    (256, 2, 256, 64, 0, M.MOE_FLAG_ROUTER_CUDA_CORE | M.MOE_FLAG_DOWN_F16)])
+def test_layer_workspace_serves_every_smaller_batch(E, k, d, F, Fs, flags):
+    dims = lambda T: M.make_dims(T, d, E, k, F, Fs, flags=flags)  # noqa: E731
+    Ts = {1, 2, 3} | set(range(1, 250000 // k, 331))
+    for t in (1024, 128 * 18, 128 * 37, 128 * 74, 4096 // k, 49152 // k, 98304 // k):
+        Ts |= {max(1, t + i) for i in (-1, 0, 1, 2)}
+    size = most = 0
+    for T in sorted(Ts):
+        most = max(most, M.workspace_size(dims(T)))
+        n = M.workspace_size_upto(dims(T))
+        assert n == most and n >= size, T
+        size = n
+    assert M.workspace_size_upto(M.make_dims(64, 100, E, k, F, Fs)) == 0
