@@ -70,14 +70,16 @@ moe_status moe_dispatch(const moe_dims_t *dims, int32_t dtype, const void *x, in
                         void *stream);
 
 /* d_x_perm [T * k, d] and add [T, d] (NULL = none) of in_dtype -> d_x [T, d] of
- * out_dtype.  d_x may be add itself (same type and stride). */
+ * out_dtype.  d_x may be add itself (MOE_ERR_INVALID_ARG then unless type and stride
+ * are the same). */
 moe_status moe_dispatch_backward(const moe_dims_t *dims, int32_t in_dtype, const void *d_x_perm,
                                  int64_t d_x_perm_stride, const int32_t *inv, const void *add,
                                  int64_t add_stride, int32_t out_dtype, void *d_x,
                                  int64_t d_x_stride, void *ws, void *stream);
 
 /* o [T * k, d] and shared [T, d] (NULL = none) of in_dtype, topk_w [T, k] fp32 ->
- * y [T, d] of out_dtype.  y may be shared itself (same type and stride). */
+ * y [T, d] of out_dtype.  y may be shared itself (MOE_ERR_INVALID_ARG then unless type
+ * and stride are the same). */
 moe_status moe_combine(const moe_dims_t *dims, int32_t in_dtype, const void *o, int64_t o_stride,
                        const int32_t *inv, const float *topk_w, const void *shared,
                        int64_t shared_stride, int32_t out_dtype, void *y, int64_t y_stride,

@@ -38,6 +38,13 @@ moe_status check_header(const void *ws) {
   return (reinterpret_cast<uintptr_t>(ws) & 255) == 0 ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
+// Output rows may replace input rows where each element takes the place of its own input
+// (same type and stride): any other way, threads would overwrite rows not yet read.
+bool in_place_ok(const void *in, int32_t in_dtype, int64_t in_stride, const void *out,
+                 int32_t out_dtype, int64_t out_stride) {
+  return in != out || (in_dtype == out_dtype && in_stride == out_stride);
+}
+
 int64_t slots(const moe_dims_t *dims) {
   return static_cast<int64_t>(dims->T) * dims->num_experts_per_tok;
 }
@@ -142,7 +149,8 @@ moe_status moe_dispatch_backward(const moe_dims_t *dims, int32_t in_dtype, const
   if (st != MOE_OK || dims->T == 0) return st;
   const int d = dims->d_model;
   if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype) || !good(d_x_perm) || !good(inv) || !good(d_x) ||
-      !aligned16(add) || d_x_perm_stride < d || d_x_stride < d || (add && add_stride < d))
+      !aligned16(add) || d_x_perm_stride < d || d_x_stride < d || (add && add_stride < d) ||
+      !in_place_ok(add, in_dtype, add_stride, d_x, out_dtype, d_x_stride))
     return MOE_ERR_INVALID_ARG;
   if ((st = check_header(ws)) != MOE_OK) return st;
   set_last_launch_count(0);
@@ -162,7 +170,8 @@ moe_status moe_combine(const moe_dims_t *dims, int32_t in_dtype, const void *o, 
   const int d = dims->d_model;
   if (!dtype_ok(in_dtype) || !dtype_ok(out_dtype) || !good(o) || !good(inv) || !good(topk_w) ||
       !good(y) || !aligned16(shared) || o_stride < d || y_stride < d ||
-      (shared && shared_stride < d))
+      (shared && shared_stride < d) ||
+      !in_place_ok(shared, in_dtype, shared_stride, y, out_dtype, y_stride))
     return MOE_ERR_INVALID_ARG;
   if ((st = check_header(ws)) != MOE_OK) return st;
   set_last_launch_count(0);
@@ -183,7 +192,7 @@ moe_status moe_combine_backward(const moe_dims_t *dims, int32_t dtype, const voi
   if (!dtype_ok(dtype) || !good(d_y) || !good(o) || !good(inv) || !good(topk_w) || !good(d_o) ||
       !good(d_topk_w) || d_y_stride < d || o_stride < d || d_o_stride < d)
     return MOE_ERR_INVALID_ARG;
-  if (d_o == o && d_o_stride != o_stride) return MOE_ERR_INVALID_ARG;
+  if (!in_place_ok(o, dtype, o_stride, d_o, dtype, d_o_stride)) return MOE_ERR_INVALID_ARG;
   if ((st = check_header(ws)) != MOE_OK) return st;
   set_last_launch_count(0);
   return launched(launch_combine_backward(dtype, d_y, d_y_stride, o, o_stride, inv, topk_w,

@@ -1,5 +1,7 @@
 """Limits of the row operators, the 8-bit products and the layers on them: sizes of
 workspaces, refused arguments (no GPU needed: these paths return before any CUDA call)."""
+import ctypes
+
 import pytest
 
 from sparse_moe_layer_select_b200 import build as B
@@ -9,6 +11,34 @@ from sparse_moe_layer_select_b200 import moe as M
 @pytest.fixture(scope="module", autouse=True)
 def _built():
     B.build()
+
+
+@pytest.fixture(scope="module")
+def L():
+    """The library with 64-bit strides and addresses (ctypes passes plain integers as 32-bit)."""
+    lib = ctypes.CDLL(M.LIB_PATH)
+    P, I, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    lib.moe_dispatch_backward.argtypes = [P, I, P, S, P, P, S, I, P, S, P, P]
+    lib.moe_combine.argtypes = [P, I, P, S, P, P, P, S, I, P, S, P, P]
+    return lib
+
+
+BAD, SHAPE = M.MOE_ERR_INVALID_ARG, M.MOE_ERR_UNSUPPORTED_SHAPE
+
+
+# ---------------------------------------------------------------- refused arguments
+
+# addend: type and stride of the rows and of the output that replaces them (no call with
+# matching ones here: it would be launched)
+@pytest.mark.parametrize("in_type,in_stride,out_type,out_stride", [
+    (0, 104, 2, 104), (0, 104, 0, 112), (2, 104, 1, 104), (1, 104, 0, 104), (2, 128, 2, 104)])
+def test_sums_in_place_need_one_type_and_stride(L, in_type, in_stride, out_type, out_stride):
+    dims = ctypes.byref(M.make_dims(64, 100, 16, 4, 0, 0))
+    rows, inv, w, out = 1 << 20, 2 << 20, 3 << 20, 4 << 20  # never dereferenced
+    assert L.moe_combine(dims, in_type, rows, 104, inv, w, out, in_stride, out_type, out,
+                         out_stride, None, None) == BAD
+    assert L.moe_dispatch_backward(dims, in_type, rows, 104, inv, out, in_stride, out_type, out,
+                                   out_stride, None, None) == BAD
 
 
 # ---------------------------------------------------------------- workspaces
