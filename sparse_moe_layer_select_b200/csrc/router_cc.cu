@@ -528,10 +528,21 @@ __device__ __forceinline__ void select_token(int t, int lane, RefineScratch *rs,
   // With a selection-only bias the rounds carried sigmoid(l) + b: the weights
   // take the selected experts' own logits.
   if (sel_bias && lane < k) my_l = row[my_e];
-  const float s = 1.f / (1.f + expf(-my_l));
+  float s = 1.f / (1.f + expf(-my_l));
   float sum = lane < k ? s : 0.f;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  // Scores near the smallest float lose their bits and then underflow (all of them: 0 / 0).
+  // With every selected score below 2^-64, sigmoid(l) is exp(l) to fp32, and its common factor
+  // drops out of the normalised weights.
+  if (norm_topk && sum < 0x1p-64f) {
+    float top = lane < k ? my_l : -INFINITY;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    sum = s = lane < k ? expf(my_l - top) : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  }
   if (lane < k) {
     const size_t o = static_cast<size_t>(t) * k + lane;
     topk_idx[o] = my_e;

@@ -3,11 +3,12 @@ than the buffers were made for, row offsets past 2^31, scores that underflow."""
 import numpy as np
 import pytest
 
+from oracle import moe_oracle as O
 from oracle import rows_oracle as R
 from sparse_moe_layer_select_b200 import inputs as I
 from sparse_moe_layer_select_b200 import moe as M
 from tests import gpu_common as G
-from tests.rows_common import dev, routing
+from tests.rows_common import dev, f64, routing
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,60 @@ def test_layer_runs_a_batch_with_more_router_planes(T, most, int8):
         ys.append(layer.forward(x))
         assert layer.device_status() == (0, 0)
     assert torch.equal(*ys)
+
+
+# ---------------------------------------------------------------- scores that underflow
+
+@pytest.mark.parametrize("flag,T", [(M.MOE_FLAG_ROUTER_CUDA_CORE, 64), (M.MOE_FLAG_ROUTER_TENSOR, 1030)])
+@pytest.mark.parametrize("selection_bias", [False, True])
+def test_router_weights_and_gradient_of_scores_that_underflow(flag, T, selection_bias):
+    """sigmoid(l) is 0 in fp32 below l = -88.7 and keeps few bits above; the normalised weights
+    of such rows are those of their logits all the same."""
+    import torch
+    E, k, d = 32, 8, 64
+    # token t has the logits of column t % d, exactly: distinct values, the largest at `top`
+    top = np.array([-20, -43, -45, -80, -87, -88.5, -89, -104, -150, -300])[np.arange(d) % 10]
+    rng = np.random.default_rng(4)
+    step = np.where(top < -128, 2.0, 0.5)
+    W = np.stack([t - s * rng.permutation(E) for t, s in zip(top, step)], 1).astype(np.float32)
+    x = np.zeros((T, d), dtype=np.float32)
+    x[np.arange(T), np.arange(T) % d] = 1.0
+    dims = M.make_dims(T, d, E, k, 64, 0, 2.5, 1,
+                       flag | (M.MOE_FLAG_BIAS_SELECTION_ONLY if selection_bias else 0))
+    xb, wb = dev(x).bfloat16(), dev(W).bfloat16()
+    assert np.array_equal(f64(wb), W)
+    bias = rng.normal(size=E).astype(np.float32) if selection_bias else None
+    ws = M.alloc_workspace(dims)
+    idx = torch.empty((T, k), dtype=torch.int32, device="cuda")
+    w = torch.empty((T, k), dtype=torch.float32, device="cuda")
+    M.route(dims, xb, wb, None if bias is None else dev(bias), idx, w, ws)
+    assert M.read_device_status(ws) == (0, 0)
+    logits = W.T.astype(np.float64)[np.arange(T) % d]
+    off = M.lib().moe_logits_offset(dims)
+    got_l = ws[off:off + 4 * T * E].view(torch.float32).view(T, E)
+    assert np.array_equal(f64(got_l), logits)
+    sel = idx.cpu().numpy()
+    if selection_bias:  # scores are nothing beside the bias, but for the rows at -20: 2e-9
+        assert np.array_equal(np.sort(sel[top[np.arange(T) % d] < -40][0]), np.sort(np.argsort(-bias)[:k]))
+    else:
+        assert np.array_equal(sel, np.argsort(-logits, axis=1, kind="stable")[:, :k])
+    l = np.take_along_axis(logits, sel.astype(np.int64), 1)
+    s = O.sigmoid(l)
+    want = s / s.sum(1, keepdims=True)
+    # a difference of two logits (exact), an exponential of two units, twice; k sums, a division.
+    # Above 2^-64 (the first two tops) the exponential's argument has no error either.
+    tol = (4 + 4 + k + 2) * 2.0 ** -24
+    assert np.all(np.abs(f64(w) - want) <= tol * want)
+    # and back
+    d_w = rng.normal(size=(T, k)).astype(np.float32)
+    out = torch.full((T, E), float("nan"), device="cuda")
+    M.route_backward(dims, got_l.contiguous(), idx, dev(d_w), out, ws)
+    ref = R.route_backward(logits, sel, d_w.astype(np.float64), 1)
+    p = R.route_weights(logits, sel, 1)
+    mag = np.zeros((T, E))
+    np.put_along_axis(mag, sel.astype(np.int64),
+                      p * (np.abs(d_w) + (np.abs(d_w) * p).sum(1, keepdims=True)), 1)
+    # (log sigmoid of magnitude |l|: |l| roundings of relative error in a weight, twice with the
+    # maximum's; some 16 operations of a step or two each)
+    worst = 16 * 2 + 4 * np.abs(logits).max(1, keepdims=True)
+    assert np.all(np.abs(f64(out) - ref) <= worst * 2.0 ** -24 * mag)
