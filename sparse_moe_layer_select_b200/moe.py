@@ -489,7 +489,10 @@ def prepare_int8(W, stream=None):
     """int8 copies of the expert weights (a model-load step): gate and up rows of each expert in
     one matrix, as moe_matmul_int8's SwiGLU form takes them.  Returns a dict of codes and scales:
     gate_up [E, 2F, d], down [E, d, F] and, with a shared expert, s_gate_up [2Fs, d] and
-    s_down [d, Fs]; "<name>_scale" has one fp32 scale per row."""
+    s_down [d, Fs]; "<name>_scale" has one fp32 scale per row.
+
+    A weight row that holds an infinity or NaN has no scale, and every output of its channel
+    would be NaN: MoeError(MOE_ERR_DEVICE_BOUNDS).  Waits for the stream."""
     import torch
 
     def rows(w):
@@ -515,6 +518,12 @@ def prepare_int8(W, stream=None):
             quantize_int8(W[name], Q["s_gate_up"][i * Fs:(i + 1) * Fs],
                           Q["s_gate_up_scale"][i * Fs:(i + 1) * Fs], stream=stream)
         Q["s_down"], Q["s_down_scale"] = rows(W["ws_down"])
+    if stream is not None:
+        stream.synchronize()
+    bad = [n for n, t in Q.items() if n.endswith("_scale") and bool(torch.isnan(t).any())]
+    if bad:
+        raise MoeError(MOE_ERR_DEVICE_BOUNDS,
+                       f"prepare_int8 (weight rows with an infinity or NaN: {', '.join(bad)})")
     return Q
 
 

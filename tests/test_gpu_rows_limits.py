@@ -125,3 +125,24 @@ def test_router_weights_and_gradient_of_scores_that_underflow(flag, T, selection
     # maximum's; some 16 operations of a step or two each)
     worst = 16 * 2 + 4 * np.abs(logits).max(1, keepdims=True)
     assert np.all(np.abs(f64(out) - ref) <= worst * 2.0 ** -24 * mag)
+
+
+# ---------------------------------------------------------------- weights without a scale
+
+@pytest.mark.parametrize("name,at,value", [("w_gate", (3, 5, 7), np.inf), ("w_up", (15, 127, 255), np.nan),
+                                           ("w_down", (0, 0, 0), -np.inf), ("ws_gate", (1, 1), np.nan),
+                                           ("ws_up", (0, 255), np.inf), ("ws_down", (255, 0), np.nan)])
+def test_int8_weights_with_an_infinity_or_nan_are_refused(name, at, value):
+    import torch
+    w = I.get("c1_tiny")
+    W = G.host_to_device(I.host_inputs(w))
+    W[name][at] = value
+    for stream in (None, torch.cuda.Stream()):
+        torch.cuda.synchronize()
+        with pytest.raises(M.MoeError) as e:
+            M.prepare_int8(W, stream)
+        assert e.value.code == M.MOE_ERR_DEVICE_BOUNDS
+    with pytest.raises(M.MoeError):
+        M.MoeLayer(W, w.d_model, w.E, w.k, w.F, w.Fs, max_tokens=8, int8=True)
+    W[name][at] = 1.0
+    M.prepare_int8(W)
