@@ -50,6 +50,10 @@ MOE_DTYPE_F32 = 2
 
 MOE_INT8_SWIGLU = 1
 
+# Flags that choose what MoeLayer(int8=True) does not have.
+INT8_REFUSED_FLAGS = (MOE_FLAG_GEMM_SINGLE_CTA | MOE_FLAG_GEMM_PAIR | MOE_FLAG_FP8_EXPERTS |
+                      MOE_FLAG_COMBINE_REDUCE | MOE_FLAG_FUSED_EXPERTS)
+
 # Expert id of a (token, slot) pair that is not routed (a padding token).
 MOE_NOT_ROUTED = -1
 
@@ -531,13 +535,17 @@ class MoeLayer:
     """A layer instance: device weights, routing buffers and workspace, reused across calls.
 
     fp8 and int8 keep 8-bit copies of the expert weights instead (one of the two): fp8 by
-    moe_forward_fp8, int8 by the row and 8-bit integer calls in a row (a token mask is taken)."""
+    moe_forward_fp8, int8 by the row and 8-bit integer calls in a row (a token mask is taken;
+    flags of the 16-bit experts' engines and combine raise ValueError)."""
 
     def __init__(self, weights: dict, d_model, num_experts, num_experts_per_tok,
                  moe_intermediate_size, shared_intermediate_size, routed_scaling_factor=2.5,
                  max_tokens=1, flags=0, device="cuda", prepare=True, fp8=False, int8=False):
         if fp8 and int8:
             raise ValueError("fp8 or int8 experts, not both")
+        if int8 and flags & INT8_REFUSED_FLAGS:
+            raise ValueError("the int8 layer has one combine and its own choice of products: "
+                             f"flags {flags & INT8_REFUSED_FLAGS} have no meaning there")
         self.W = dict(weights)
         self.cfg = dict(d_model=d_model, num_experts=num_experts,
                         num_experts_per_tok=num_experts_per_tok,

@@ -41,6 +41,17 @@ def test_sums_in_place_need_one_type_and_stride(L, in_type, in_stride, out_type,
                                    out_stride, None, None) == BAD
 
 
+@pytest.mark.parametrize("flag", [M.MOE_FLAG_GEMM_SINGLE_CTA, M.MOE_FLAG_GEMM_PAIR,
+                                  M.MOE_FLAG_FP8_EXPERTS, M.MOE_FLAG_COMBINE_REDUCE,
+                                  M.MOE_FLAG_FUSED_EXPERTS])
+def test_int8_layer_refuses_flags_it_has_no_use_for(flag):
+    for flags in (flag, flag | M.MOE_FLAG_ROUTER_TENSOR):
+        with pytest.raises(ValueError, match="flags"):  # before the (missing) weights are read
+            M.MoeLayer({}, 256, 16, 4, 128, 128, flags=flags, int8=True)
+    with pytest.raises(KeyError):
+        M.MoeLayer({}, 256, 16, 4, 128, 128, flags=M.MOE_FLAG_ROUTER_TENSOR, int8=True)
+
+
 # ---------------------------------------------------------------- workspaces
 
 def _chunks(n):
