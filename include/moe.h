@@ -173,6 +173,10 @@ size_t moe_workspace_size(const moe_dims_t *dims);
  * in steps as T grows.) */
 size_t moe_workspace_size_upto(const moe_dims_t *dims);
 
+/* Bytes that moe_route and moe_route_masked need, for every batch of up to dims->T
+ * tokens: the part of the workspace up to the end of the logits. */
+size_t moe_route_workspace_size(const moe_dims_t *dims);
+
 /* Router: sigmoid scores, top-k with ties to the lower expert index, and
  * post-top-k normalisation (Laguna M.1/XS.2 Technical Report summary, Key
  * claims, report §3.1; Laguna-M.1-base spec sheet, Mixture of experts: the

@@ -217,6 +217,27 @@ WsLayout ws_layout(const Dims &D) {
   return L;
 }
 
+constexpr size_t WsLayout::*kRouteEnd = &WsLayout::inv;  // what the router uses ends there
+
+// The largest value of a section's offset (or of the total) over all batches of up to D.T
+// tokens.  Every section grows with T except where the index's chunks double and where the
+// router takes fewer K slices: besides D.T itself, the last batches before those steps.
+size_t largest_upto(Dims D, size_t WsLayout::*what) {
+  size_t most = ws_layout(D).*what;
+  static_assert(4 * kIndexChunkMin == kIndexChunk, "two steps of the chunk size");
+  const int64_t steps[] = {
+      int64_t(kIndexChunkMin) * kIndexChunksWanted / D.k,
+      int64_t(2 * kIndexChunkMin) * kIndexChunksWanted / D.k, kRouterSplitSms / 8 * kBlockM,
+      kRouterSplitSms / 4 * kBlockM, kRouterSplitSms / 2 * kBlockM};
+  const int T = D.T;
+  for (const int64_t t : steps) {
+    if (t >= T) continue;
+    D.T = static_cast<int>(t);
+    most = std::max(most, ws_layout(D).*what);
+  }
+  return most;
+}
+
 // Width of one part of an FFN of width f in the fused kernel: f split into the
 // fewest equal parts of at most 512 columns (and at least min_parts parts, as
 // far as parts of whole 128-column chunks allow); 0 if no such split exists.
@@ -275,9 +296,10 @@ moe_status check_router_dims(const Dims &D) {
 
 inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-moe_status check_ws(const Dims &D, const void *ws, size_t ws_bytes) {
+moe_status check_ws(const Dims &D, const void *ws, size_t ws_bytes,
+                    size_t WsLayout::*end = &WsLayout::total) {
   if (ws == nullptr || (reinterpret_cast<uintptr_t>(ws) & 255) != 0) return MOE_ERR_INVALID_ARG;
-  if (ws_bytes < ws_layout(D).total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+  if (ws_bytes < ws_layout(D).*end) return MOE_ERR_WORKSPACE_TOO_SMALL;
   return MOE_OK;
 }
 
@@ -436,21 +458,12 @@ size_t moe_workspace_size(const moe_dims_t *dims) {
 
 size_t moe_workspace_size_upto(const moe_dims_t *dims) {
   Dims D;
-  if (check_dims(dims, &D) != MOE_OK) return 0;
-  size_t most = ws_layout(D).total;
-  // Every section grows with T except where the index's chunks double and where the router
-  // takes fewer K slices: the last batches before those steps are the others to look at.
-  const int64_t steps[] = {
-      int64_t(kIndexChunkMin) * kIndexChunksWanted / D.k,
-      int64_t(2 * kIndexChunkMin) * kIndexChunksWanted / D.k, kRouterSplitSms / 8 * kBlockM,
-      kRouterSplitSms / 4 * kBlockM, kRouterSplitSms / 2 * kBlockM};
-  static_assert(4 * kIndexChunkMin == kIndexChunk, "two steps of the chunk size");
-  for (const int64_t t : steps) {
-    if (t >= dims->T) continue;
-    D.T = static_cast<int>(t);
-    most = std::max(most, ws_layout(D).total);
-  }
-  return most;
+  return check_dims(dims, &D) == MOE_OK ? largest_upto(D, &WsLayout::total) : 0;
+}
+
+size_t moe_route_workspace_size(const moe_dims_t *dims) {
+  Dims D;
+  return check_dims(dims, &D) == MOE_OK ? largest_upto(D, kRouteEnd) : 0;
 }
 
 moe_status moe_route(const moe_dims_t *dims, const void *x, const void *w_router,
@@ -472,7 +485,7 @@ moe_status moe_route_masked(const moe_dims_t *dims, const void *x, const void *w
   if (!aligned16(x) || !aligned16(w_router) || !aligned16(topk_idx) || !aligned16(topk_w) ||
       (router_bias && !aligned16(router_bias)))
     return MOE_ERR_INVALID_ARG;
-  if ((st = check_ws(D, ws, ws_bytes)) != MOE_OK) return st;
+  if ((st = check_ws(D, ws, ws_bytes, kRouteEnd)) != MOE_OK) return st;
   g_last_launches = 0;
   if (D.T == 0) return MOE_OK;
   int sms = 0;

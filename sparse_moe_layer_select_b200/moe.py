@@ -33,7 +33,8 @@ MOE_FLAG_COMBINE_REDUCE = 128
 MOE_FLAG_FUSED_EXPERTS = 256
 
 # Every symbol the header declares (checked by the CPU tests).
-EXPORTED = ["moe_workspace_size", "moe_workspace_size_upto", "moe_route", "moe_permute", "moe_forward",
+EXPORTED = ["moe_workspace_size", "moe_workspace_size_upto", "moe_route_workspace_size",
+            "moe_route", "moe_permute", "moe_forward",
             "moe_read_device_status", "moe_selftest_bounded_wait", "moe_status_string",
             "moe_last_launch_count", "moe_profile_next_forward", "moe_prepare_down_f16",
             "moe_logits_offset", "moe_permute_static", "moe_route_masked",
@@ -119,6 +120,8 @@ def lib():
         L.moe_workspace_size.argtypes = [D]
         L.moe_workspace_size_upto.restype = ctypes.c_size_t
         L.moe_workspace_size_upto.argtypes = [D]
+        L.moe_route_workspace_size.restype = ctypes.c_size_t
+        L.moe_route_workspace_size.argtypes = [D]
         L.moe_route.restype = ctypes.c_int
         L.moe_route.argtypes = [D, P, P, P, P, P, P, ctypes.c_size_t, P]
         L.moe_permute.restype = ctypes.c_int
@@ -201,13 +204,28 @@ def workspace_size_upto(dims) -> int:
     return int(lib().moe_workspace_size_upto(ctypes.byref(dims)))
 
 
+def route_workspace_size(dims) -> int:
+    """What the router alone needs, for every batch of up to dims.T tokens."""
+    return int(lib().moe_route_workspace_size(ctypes.byref(dims)))
+
+
+def _workspace(n, name, device):
+    import torch
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, name)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def alloc_workspace(dims, device="cuda", upto=False):
     """A workspace for these dims, or (upto) for every batch of up to dims.T tokens."""
-    import torch
-    n = workspace_size_upto(dims) if upto else workspace_size(dims)
-    if n == 0:
-        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_workspace_size")
-    return torch.empty(n, dtype=torch.uint8, device=device)
+    if upto:
+        return _workspace(workspace_size_upto(dims), "moe_workspace_size_upto", device)
+    return _workspace(workspace_size(dims), "moe_workspace_size", device)
+
+
+def alloc_route_workspace(dims, device="cuda"):
+    """A workspace for moe_route alone, for every batch of up to dims.T tokens."""
+    return _workspace(route_workspace_size(dims), "moe_route_workspace_size", device)
 
 
 def route(dims, x, w_router, bias, topk_idx, topk_w, ws, stream=None, token_mask=None):
@@ -534,9 +552,10 @@ def prepare_int8(W, stream=None):
 class MoeLayer:
     """A layer instance: device weights, routing buffers and workspace, reused across calls.
 
-    fp8 and int8 keep 8-bit copies of the expert weights instead (one of the two): fp8 by
-    moe_forward_fp8, int8 by the row and 8-bit integer calls in a row (a token mask is taken;
-    flags of the 16-bit experts' engines and combine raise ValueError)."""
+    fp8 or int8 (one of the two) make 8-bit copies of the expert weights.  fp8 runs
+    moe_forward_fp8; int8 runs the row and 8-bit integer calls one after another, and keeps
+    the copies instead of the weights (a token mask is taken; flags of the 16-bit experts'
+    engines and combine raise ValueError)."""
 
     def __init__(self, weights: dict, d_model, num_experts, num_experts_per_tok,
                  moe_intermediate_size, shared_intermediate_size, routed_scaling_factor=2.5,
@@ -559,6 +578,7 @@ class MoeLayer:
             if workspace_size(self.dims(1)) == 0:
                 raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_workspace_size")
             self.int8 = prepare_int8(self.W)
+            self.W = {n: self.W.get(n) for n in ("w_router", "router_bias")}
         elif fp8:  # one-time FP8 copies of the expert weights (model-load step)
             self.cfg["flags"] |= MOE_FLAG_FP8_EXPERTS
             self.fp8, (code, site) = prepare_fp8(self.dims(1), self.W)
@@ -582,7 +602,10 @@ class MoeLayer:
     def _reserve(self, T):
         self.max_tokens = T
         d = self.dims(T)
-        self.ws = alloc_workspace(d, self.device, upto=True)
+        if self.int8 is not None:  # self.ws is the router's
+            self.ws = alloc_route_workspace(d, self.device)
+        else:
+            self.ws = alloc_workspace(d, self.device, upto=True)
         self.routing = alloc_routing(d, self.device)
         self._r_struct = routing_struct(self.routing)
         if self.int8 is not None:

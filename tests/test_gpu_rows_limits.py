@@ -146,3 +146,40 @@ def test_int8_weights_with_an_infinity_or_nan_are_refused(name, at, value):
         M.MoeLayer(W, w.d_model, w.E, w.k, w.F, w.Fs, max_tokens=8, int8=True)
     W[name][at] = 1.0
     M.prepare_int8(W)
+
+
+# ---------------------------------------------------------------- what a layer holds
+
+@pytest.mark.parametrize("T,flag", [(64, 0), (2304, M.MOE_FLAG_ROUTER_TENSOR), (9473, 0)])
+def test_router_writes_nothing_behind_its_workspace(T, flag):
+    import torch
+    w = I.get("c1_tiny").with_(T=T, num_experts=256, num_experts_per_tok=2)
+    h = G.host_to_device(I.host_inputs(w))
+    dims = M.dims_for(w, flags=flag)
+    n = M.route_workspace_size(dims)
+    whole = torch.full((n + 4096,), 0xAB, dtype=torch.uint8, device="cuda")
+    outs = []
+    for ws in (whole[:n], M.alloc_workspace(dims)):
+        idx = torch.empty((T, w.k), dtype=torch.int32, device="cuda")
+        wt = torch.empty((T, w.k), device="cuda")
+        M.route(dims, h["x"], h["w_router"], None, idx, wt, ws)
+        assert M.read_device_status(ws) == (0, 0)
+        outs.append((idx, wt))
+    assert torch.all(whole[n:] == 0xAB)
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+def test_int8_layer_holds_its_codes_and_not_the_weights():
+    import torch
+    w = I.get("c1_tiny")
+    W = G.host_to_device(I.host_inputs(w))
+    layer = M.MoeLayer(W, w.d_model, w.E, w.k, w.F, w.Fs, max_tokens=w.T, int8=True)
+    assert layer.ws.numel() == M.route_workspace_size(layer.dims(w.T))
+    assert layer.ws.numel() < M.workspace_size(layer.dims(w.T)) / 10
+    x = W["x"]
+    first = layer.forward(x)
+    for n in G.WEIGHT_KEYS[1:]:  # gone or overwritten by their owner, to no effect
+        W[n].fill_(float("nan"))
+    W.clear()
+    assert sorted(n for n, t in layer.W.items() if t is not None) == ["w_router"]
+    assert torch.equal(layer.forward(x), first) and layer.device_status() == (0, 0)

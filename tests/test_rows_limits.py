@@ -97,10 +97,27 @@ def test_layer_workspace_serves_every_smaller_batch(E, k, d, F, Fs, flags):
     Ts = {1, 2, 3} | set(range(1, 250000 // k, 331))
     for t in (1024, 128 * 18, 128 * 37, 128 * 74, 4096 // k, 49152 // k, 98304 // k):
         Ts |= {max(1, t + i) for i in (-1, 0, 1, 2)}
-    size = most = 0
+    size = most = route = 0
     for T in sorted(Ts):
         most = max(most, M.workspace_size(dims(T)))
+        # the router alone: header, index and logits, whatever follows them
+        planes = (M.lib().moe_logits_offset(dims(T)) + 255) // 256 * 256 + 4 * T * E
+        n = M.route_workspace_size(dims(T))
+        assert max(planes, route) <= n <= M.workspace_size_upto(dims(T)), T
+        route = n
         n = M.workspace_size_upto(dims(T))
         assert n == most and n >= size, T
         size = n
     assert M.workspace_size_upto(M.make_dims(64, 100, E, k, F, Fs)) == 0
+    assert M.route_workspace_size(M.make_dims(64, 100, E, k, F, Fs)) == 0
+
+
+def test_router_needs_no_room_for_the_experts(L):
+    dims = M.make_dims(64, 2048, 256, 8, 512, 512)
+    # header, histogram and tile lists, logits: no fp16 copy of the weights (537 MB)
+    assert M.route_workspace_size(dims) < 200_000 < 500_000_000 < M.workspace_size(dims)
+    n = M.route_workspace_size(M.make_dims(32768, 2048, 256, 8, 512, 512))
+    assert n < 40_000_000
+    L.moe_route.argtypes = [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]
+    assert L.moe_route(ctypes.byref(dims), 1 << 20, 2 << 20, None, 3 << 20, 4 << 20, 5 << 20,
+                       M.route_workspace_size(dims) - 1, None) == M.MOE_ERR_WORKSPACE_TOO_SMALL
