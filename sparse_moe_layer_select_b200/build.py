@@ -2,13 +2,18 @@
 
   libmoe_b200.so    the MoE layer (C ABI of include/moe.h and include/moe_rows.h)
   libmoe_gen.so     the seeded input generator (test and benchmark inputs only)
-  _rows_binding.so  argument marshalling of the row and 8-bit integer calls (CPython module)
+  _rows_binding.so  argument marshalling of the row and 8-bit integer calls (CPython module;
+                    left out where torch, Python's headers or g++ are missing: programs of the
+                    C ABI need none of them)
 
 Usage: python -m sparse_moe_layer_select_b200.build   (or build() from Python)
 """
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -53,15 +58,27 @@ def _build_lib(name, sources, extra=(), force=False, verbose=False):
     return out
 
 
+def _binding_lacks():
+    """What the binding needs and is not here, or None."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    return None if shutil.which("g++") else "g++"
+
+
 def _build_binding(force=False, verbose=False):
     """The CPython module over the C ABI (it reads torch tensors, so it needs torch's headers)."""
+    lacks = _binding_lacks()
+    if lacks:
+        print(f"_rows_binding.so not built: no {lacks} (moe.py's row and 8-bit integer calls "
+              "need it)", file=sys.stderr)
+        return None
     out = os.path.join(PKG, "_rows_binding.so")
     src = os.path.join(CSRC, "rows_binding.cpp")
     if not force and not _newer(out, [src, *(os.path.join(ROOT, "include", h)
                                            for h in ("moe.h", "moe_rows.h"))]):
         return out
-    import sysconfig
-
     import torch
     from torch.utils import cpp_extension
     inc = [f"-I{d}" for d in cpp_extension.include_paths()]

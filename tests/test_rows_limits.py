@@ -1,6 +1,7 @@
 """Limits of the row operators, the 8-bit products and the layers on them: sizes of
 workspaces, refused arguments (no GPU needed: these paths return before any CUDA call)."""
 import ctypes
+import os
 
 import pytest
 
@@ -121,3 +122,32 @@ def test_router_needs_no_room_for_the_experts(L):
     L.moe_route.argtypes = [ctypes.c_void_p] * 7 + [ctypes.c_size_t, ctypes.c_void_p]
     assert L.moe_route(ctypes.byref(dims), 1 << 20, 2 << 20, None, 3 << 20, 4 << 20, 5 << 20,
                        M.route_workspace_size(dims) - 1, None) == M.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
+# ---------------------------------------------------------------- building
+
+@pytest.mark.parametrize("missing", ["torch", "Python.h", "g++"])
+def test_libraries_build_where_the_binding_cannot(missing, monkeypatch, capsys):
+    run = []
+    monkeypatch.setattr(B.subprocess, "run", lambda cmd, check: run.append(cmd))
+    monkeypatch.setattr(B.os, "replace", lambda a, b: None)
+    if missing == "torch":
+        find = B.importlib.util.find_spec
+        monkeypatch.setattr(B.importlib.util, "find_spec",
+                            lambda n: None if n == "torch" else find(n))
+    elif missing == "Python.h":
+        monkeypatch.setattr(B.sysconfig, "get_paths", lambda: {"include": "/nowhere"})
+    else:
+        monkeypatch.setattr(B.shutil, "which", lambda n: None)
+    moe, gen = B.build(force=True)
+    assert moe.endswith("libmoe_b200.so") and gen.endswith("libmoe_gen.so")
+    assert len(run) == 2 and all("nvcc" in cmd[0] for cmd in run)
+    assert f"no {missing}" in capsys.readouterr().err
+
+
+def test_binding_is_built_where_it_can_be(monkeypatch):
+    run = []
+    monkeypatch.setattr(B.subprocess, "run", lambda cmd, check: run.append(cmd))
+    monkeypatch.setattr(B.os, "replace", lambda a, b: None)
+    B.build(force=True)
+    assert [os.path.basename(cmd[0]) for cmd in run] == ["nvcc", "nvcc", "g++"]
