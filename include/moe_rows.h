@@ -30,8 +30,9 @@ extern "C" {
  *
  * Conventions of these calls, where they differ from the ones above:
  * - dims supplies T, d_model, num_experts, num_experts_per_tok,
- *   routed_scaling_factor and norm_topk_prob; any d_model >= 1 (the widths F
- *   and Fs and the flags are ignored).  E <= 512, k <= min(E, 16) hold.
+ *   routed_scaling_factor and norm_topk_prob; any d_model from 1 to 2^30 (the
+ *   widths F and Fs and the flags are ignored).  E <= 512, k <= min(E, 16) hold;
+ *   T * k <= 2^31 - 4097.
  * - Row matrices are bf16, fp16 or fp32 (moe_dtype) with a row stride in
  *   elements (>= d_model); 16-byte-aligned bases.  Rows whose stride is no
  *   multiple of 16 bytes are taken, more slowly.
@@ -112,7 +113,7 @@ moe_status moe_route_backward(const moe_dims_t *dims, const float *logits, const
  * moe_prepare_fp8 does for e4m3.  A row that holds an infinity or NaN gets the
  * scale NaN and codes 0, so that every product of it is NaN. */
 
-/* x [rows, cols] of `dtype` (row stride in elements) -> codes (row stride in
+/* x [rows, cols] (cols <= 2^30) of `dtype` (row stride in elements) -> codes (row stride in
  * bytes, a multiple of 16; the bytes past cols are not written) and scales
  * [rows].  n_rows (device, NULL = rows): only the first *n_rows rows are
  * quantized, the others left as they were. */

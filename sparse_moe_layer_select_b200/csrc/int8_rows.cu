@@ -178,7 +178,7 @@ cudaError_t launch_shape(const void *x, int64_t x_stride, int rows, const int32_
                          float *scales, int *status, cudaStream_t s) {
   constexpr int kBlock = TPR < 128 ? 128 : TPR;
   const int chunks = (d + N - 1) / N;
-  const unsigned grid = (rows + kBlock / TPR - 1) / (kBlock / TPR);
+  const unsigned grid = (static_cast<unsigned>(rows) + kBlock / TPR - 1) / (kBlock / TPR);
   const T *xp = static_cast<const T *>(x);
   return launch_early(inv != nullptr ? quantize_kernel<T, N, TPR, R, KEEP, true>
                                      : quantize_kernel<T, N, TPR, R, KEEP, false>,

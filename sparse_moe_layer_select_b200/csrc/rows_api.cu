@@ -22,14 +22,19 @@ inline bool good(const void *p) { return p != nullptr && aligned16(p); }
 inline bool dtype_ok(int32_t t) { return t >= MOE_DTYPE_BF16 && t <= MOE_DTYPE_F32; }
 inline size_t a256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-// The dims of calls that only move rows: T, d_model, E and k; any d_model.
+// The longest row: element and chunk numbers are 32-bit on the device, and loops step past
+// the row's end.
+constexpr int kMaxRow = 1 << 30;
+
+// The dims of calls that only move rows: T, d_model, E and k.
 moe_status check_rows(const moe_dims_t *dims) {
   if (dims == nullptr || dims->struct_size != sizeof(moe_dims_t)) return MOE_ERR_INVALID_ARG;
   const int k = dims->num_experts_per_tok, E = dims->num_experts;
   if (dims->T < 0) return MOE_ERR_INVALID_ARG;
-  if (dims->d_model < 1) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (dims->d_model < 1 || dims->d_model > kMaxRow) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (E < 1 || E > 512 || k < 1 || k > 16 || k > E) return MOE_ERR_UNSUPPORTED_SHAPE;
-  if (static_cast<int64_t>(dims->T) * k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+  // (slot numbers are 32-bit, and the index rounds them up to whole chunks)
+  if (static_cast<int64_t>(dims->T) * k > INT32_MAX - kIndexChunk) return MOE_ERR_UNSUPPORTED_SHAPE;
   return MOE_OK;
 }
 
@@ -222,7 +227,7 @@ moe_status moe_quantize_int8(int32_t rows, int32_t cols, int32_t dtype, const vo
                              int64_t x_stride, const int32_t *n_rows, int8_t *codes,
                              int64_t codes_stride, float *scales, void *stream) {
   if (rows < 0 || !dtype_ok(dtype)) return MOE_ERR_INVALID_ARG;
-  if (cols < 1) return MOE_ERR_UNSUPPORTED_SHAPE;
+  if (cols < 1 || cols > kMaxRow) return MOE_ERR_UNSUPPORTED_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!good(x) || !good(codes) || !good(scales) || (reinterpret_cast<uintptr_t>(n_rows) & 3) ||
       x_stride < cols || codes_stride < cols || codes_stride % 16 != 0)

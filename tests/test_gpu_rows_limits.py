@@ -183,3 +183,19 @@ def test_int8_layer_holds_its_codes_and_not_the_weights():
     W.clear()
     assert sorted(n for n, t in layer.W.items() if t is not None) == ["w_router"]
     assert torch.equal(layer.forward(x), first) and layer.device_status() == (0, 0)
+
+
+# ---------------------------------------------------------------- past 32 bits
+
+def test_quantize_of_nearly_2_to_31_rows():
+    import torch
+    n = (1 << 31) - 2
+    x = torch.ones(n, 1, dtype=torch.bfloat16, device="cuda")
+    x[-3:, 0] = torch.tensor([2.0, -4.0, 0.0])
+    q, s = M.alloc_codes(n, 1)
+    s.fill_(-1.0)
+    M.quantize_int8(x, q, s)
+    one = np.float32(1) / np.float32(127)
+    assert int((s == float(one)).sum()) == n - 3
+    assert q[-4:, 0].tolist() == [127, 127, -127, 0]
+    assert s[-4:].tolist() == [one, np.float32(2) / np.float32(127), np.float32(4) / np.float32(127), 1.0]

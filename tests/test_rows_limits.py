@@ -21,6 +21,10 @@ def L():
     P, I, S = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
     lib.moe_dispatch_backward.argtypes = [P, I, P, S, P, P, S, I, P, S, P, P]
     lib.moe_combine.argtypes = [P, I, P, S, P, P, P, S, I, P, S, P, P]
+    lib.moe_combine_backward.argtypes = [P, I, P, S, P, S, P, P, P, S, P, P, P]
+    lib.moe_dispatch.argtypes = [P, I, P, S, P, P, S, P, P]
+    lib.moe_dispatch_int8.argtypes = [P, I, P, S, P, P, S, P, P, P]
+    lib.moe_quantize_int8.argtypes = [I, I, I, P, S, P, P, S, P, P]
     return lib
 
 
@@ -40,6 +44,23 @@ def test_sums_in_place_need_one_type_and_stride(L, in_type, in_stride, out_type,
                          out_stride, None, None) == BAD
     assert L.moe_dispatch_backward(dims, in_type, rows, 104, inv, out, in_stride, out_type, out,
                                    out_stride, None, None) == BAD
+
+
+@pytest.mark.parametrize("T,d", [(1, (1 << 31) - 1), (1, (1 << 30) + 1), (((1 << 31) - 1) // 4, 1),
+                                 ((1 << 29) - 1024, 1)])
+def test_sizes_past_32_bit_numbers_are_refused(L, T, d):
+    dims = ctypes.byref(M.make_dims(T, d, 16, 4, 0, 0))
+    s = d + 16 - d % 16
+    a = [i << 40 for i in range(1, 9)]  # never dereferenced
+    assert L.moe_dispatch(dims, 0, a[0], s, a[1], a[2], s, None, None) == SHAPE
+    assert L.moe_combine(dims, 0, a[0], s, a[1], a[2], None, 0, 0, a[3], s, None, None) == SHAPE
+    assert L.moe_dispatch_backward(dims, 0, a[0], s, a[1], None, 0, 0, a[2], s, None, None) == SHAPE
+    assert L.moe_combine_backward(dims, 0, a[0], s, a[1], s, a[2], a[3], a[4], s, a[5], None,
+                                  None) == SHAPE
+    assert L.moe_dispatch_int8(dims, 0, a[0], s, a[1], a[2], s, a[3], None, None) == SHAPE
+    assert M.sort_workspace_size(M.make_dims(T, d, 16, 4, 0, 0)) == 0
+    if T == 1:
+        assert L.moe_quantize_int8(1, d, 0, a[0], s, None, a[1], s, a[2], None) == SHAPE
 
 
 @pytest.mark.parametrize("flag", [M.MOE_FLAG_GEMM_SINGLE_CTA, M.MOE_FLAG_GEMM_PAIR,
