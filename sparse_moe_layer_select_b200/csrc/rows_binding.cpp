@@ -62,12 +62,18 @@ struct Args {
       throw Refused("the tensors are not on the current device");
     if (none(i)) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(device)).stream();
     PyObject *v = PyObject_GetAttrString(a[i], "cuda_stream");
-    if (v == nullptr) {
+    void *s = v != nullptr ? PyLong_AsVoidPtr(v) : nullptr;
+    Py_XDECREF(v);
+    if (PyErr_Occurred()) {
       PyErr_Clear();
       refuse("stream", "not a CUDA stream");
     }
-    void *s = PyLong_AsVoidPtr(v);
-    Py_DECREF(v);
+    // (torch's streams name their device; others are taken as they are)
+    PyObject *d = PyObject_GetAttrString(a[i], "device_index");
+    const long on = d != nullptr ? PyLong_AsLong(d) : device;
+    Py_XDECREF(d);
+    PyErr_Clear();
+    if (device >= 0 && on != device) refuse("stream", "of another device than the tensors");
     return s;
   }
 };

@@ -185,6 +185,35 @@ def test_int8_layer_holds_its_codes_and_not_the_weights():
     assert torch.equal(layer.forward(x), first) and layer.device_status() == (0, 0)
 
 
+# ---------------------------------------------------------------- streams
+
+def test_stream_arguments():
+    """What is no stream of the tensors' device is refused, with no error left behind."""
+    import types
+
+    import torch
+    x = torch.ones(4, 64, device="cuda")
+    q, s = M.alloc_codes(4, 64)
+    raw = torch.cuda.Stream().cuda_stream
+    new = types.SimpleNamespace
+    for bad in (0, "stream", new(), new(cuda_stream="0"), new(cuda_stream=None), new(cuda_stream=1.5),
+                new(cuda_stream=raw, device_index=1)):
+        s.fill_(-1.0)
+        torch.cuda.synchronize()
+        with pytest.raises(M.MoeError) as e:
+            M.quantize_int8(x, q, s, stream=bad)
+        assert e.value.code == M.MOE_ERR_INVALID_ARG and "stream" in str(e.value)
+        torch.cuda.synchronize()
+        assert torch.all(s == -1.0)  # nothing was launched
+    for good in (None, torch.cuda.Stream(), new(cuda_stream=raw), new(cuda_stream=raw, device_index=0),
+                 torch.cuda.default_stream()):
+        s.fill_(-1.0)
+        torch.cuda.synchronize()
+        M.quantize_int8(x, q, s, stream=good)
+        torch.cuda.synchronize()
+        assert torch.all(s > 0) and torch.all(q == 127)
+
+
 # ---------------------------------------------------------------- past 32 bits
 
 def test_quantize_of_nearly_2_to_31_rows():
