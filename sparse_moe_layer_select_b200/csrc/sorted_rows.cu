@@ -388,7 +388,6 @@ cudaError_t launch_to_tokens(int in_type, const void *o, int64_t o_stride, const
                                          : to_tokens_kernel<TI, TO, N, false>,
                             grid, kThreads, 0, s, 0, op, o_stride, ap, add_stride, inv, w, T, k, d,
                             chunks, scale, yp, y_stride, status);
-        return cudaGetLastError();
       });
     });
   });
@@ -418,8 +417,7 @@ cudaError_t launch_route_backward(const float *logits, const int32_t *topk_idx, 
                                   cudaStream_t s) {
   const unsigned grid = all_blocks(static_cast<int64_t>(T) * 16);
   return launch_early(E % 4 == 0 ? route_backward_kernel<4> : route_backward_kernel<1>, grid,
-                      kThreads, 0, s, 0, logits, topk_idx, d_w, T, E, k, norm,
-                                                       d_logits, status);
+                      kThreads, 0, s, 0, logits, topk_idx, d_w, T, E, k, norm, d_logits, status);
 }
 
 }  // namespace moe
