@@ -185,6 +185,38 @@ def test_int8_layer_holds_its_codes_and_not_the_weights():
     assert torch.equal(layer.forward(x), first) and layer.device_status() == (0, 0)
 
 
+# ---------------------------------------------------------------- the activation's error
+
+@pytest.mark.parametrize("rows,grouped", [(16, False), (255, False), (255, True)])
+def test_swiglu_error_in_units_of_the_last_place(rows, grouped):
+    """The stated bound of silu, on each of the three product kernels: gates of -126 to 126 in
+    steps of 1/128 and up values, all exact, so that only the activation and one product round."""
+    import torch
+    a = np.linspace(-127, 127, rows).round().astype(np.int8)[:, None]
+    N = 127
+    b = np.concatenate([np.arange(1, N + 1), np.ones(N)]).astype(np.int8)[:, None]
+    qa, sa = M.alloc_codes(rows, 1)
+    qb, sb = M.alloc_codes(2 * N, 1)
+    qa.copy_(dev(a)), qb.copy_(dev(b))
+    sa.fill_(1.0)
+    sb.fill_(2.0 ** -7)
+    out = torch.empty(rows, N, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    if grouped:
+        offsets = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+        M.matmul_int8(qa, sa, qb[None], sb, out, ws, offsets=offsets, swiglu=True)
+    else:
+        M.matmul_int8(qa, sa, qb, sb, out, ws, swiglu=True)
+    assert M.read_device_status(ws) == (0, 0)
+    gate, up, got = a / 128.0 * b[:N].T.astype(np.float64), a / 128.0, f64(out)
+    want = gate * R.sigmoid(gate) * up
+    units = np.where(gate < 0, 5 + 1.2 * np.abs(gate), 6) + 0.5
+    on = gate > -87
+    # (a unit is at most 2^-23 of the value, and 2^-149 near zero)
+    assert np.all(np.abs(got - want)[on] <= (units * 2.0 ** -23 * np.abs(want) + 2.0 ** -149)[on])
+    assert np.all(got[gate < -88] == 0)
+
+
 # ---------------------------------------------------------------- streams
 
 def test_stream_arguments():
