@@ -606,6 +606,7 @@ class MoeLayer:
             self.ws = alloc_route_workspace(d, self.device)
         else:
             self.ws = alloc_workspace(d, self.device, upto=True)
+        self.ws[:256].zero_()  # the status that device_status() reads before a first forward
         self.routing = alloc_routing(d, self.device)
         self._r_struct = routing_struct(self.routing)
         if self.int8 is not None:
@@ -619,7 +620,9 @@ class MoeLayer:
 
             def buffers(rows, F):
                 # the activation stays in fp32 up to its codes: rounded to fp16 first, codes near
-                # a border would move
+                # a border would move.  The experts' outputs are rounded to fp16 (2^-11 of each
+                # at most, an eighth of the sum's own rounding to bf16), as the 16-bit layer's are: half
+                # the bytes that the product writes and the combine reads
                 b = {"h": new(rows, F, dtype=torch.float32),
                      "o": new(rows, c["d_model"], dtype=torch.float16)}
                 b["xq"], b["xs"] = alloc_codes(rows, c["d_model"], self.device)
@@ -658,7 +661,8 @@ class MoeLayer:
         combine(d, b["o"], out["inv"], w, y, self.ws, shared, stream)
 
     def device_status(self, stream=None):
-        """(code, site) of the first device-side error of the last forward (synchronises)."""
+        """(code, site) of the first device-side error of the last forward that had tokens
+        (synchronises)."""
         status = read_device_status(self.ws, stream)
         if status[0] == MOE_OK and self.int8 is not None:
             status = read_device_status(self._sort_ws, stream)

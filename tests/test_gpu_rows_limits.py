@@ -169,6 +169,19 @@ def test_router_writes_nothing_behind_its_workspace(T, flag):
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
 
 
+@pytest.mark.parametrize("kind", [{}, {"fp8": True}, {"int8": True}])
+def test_device_status_before_a_first_batch(kind):
+    import torch
+    w = I.get("c1_tiny")
+    W = G.host_to_device(I.host_inputs(w))
+    new = lambda: M.MoeLayer(W, w.d_model, w.E, w.k, w.F, w.Fs, max_tokens=64, **kind)  # noqa: E731
+    layer = new()
+    layer.ws.fill_(0xFF)  # its memory goes back and is given to the next layer
+    del layer
+    layer = new()
+    assert layer.device_status() == (0, 0)
+
+
 def test_int8_layer_holds_its_codes_and_not_the_weights():
     import torch
     w = I.get("c1_tiny")
