@@ -675,13 +675,14 @@ class MoeLayer:
             self._reserve(T)
         if y is None:
             y = torch.empty_like(x)
+        if self.fp8 is not None and token_mask is not None:
+            raise ValueError("the FP8-expert forward takes no token mask")
+        if T == 0:  # (an empty tensor has no address to pass on)
+            return y
         d = self.dims(T)
         if self.int8 is not None:
-            if T > 0:
-                self._forward_int8(d, x, y, stream, token_mask)
+            self._forward_int8(d, x, y, stream, token_mask)
         elif self.fp8 is not None:
-            if token_mask is not None:
-                raise ValueError("the FP8-expert forward takes no token mask")
             forward_fp8(d, self._ws_struct, self._q_struct, x, y, self._r_struct, self.ws, stream)
         else:
             forward(d, self._ws_struct, x, y, self._r_struct, self.ws, stream,

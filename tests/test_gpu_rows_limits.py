@@ -182,6 +182,19 @@ def test_device_status_before_a_first_batch(kind):
     assert layer.device_status() == (0, 0)
 
 
+@pytest.mark.parametrize("kind", [{}, {"fp8": True}, {"int8": True}])
+def test_layers_take_no_tokens(kind):
+    import torch
+    w = I.get("c1_tiny")
+    W = G.host_to_device(I.host_inputs(w))
+    layer = M.MoeLayer(W, w.d_model, w.E, w.k, w.F, w.Fs, max_tokens=64, **kind)
+    before = layer.forward(W["x"])
+    assert layer.forward(W["x"][:0]).shape == (0, w.d_model)
+    y = torch.empty(0, w.d_model, dtype=torch.bfloat16, device="cuda")
+    assert layer.forward(W["x"][:0], y) is y
+    assert torch.equal(layer.forward(W["x"]), before) and layer.device_status() == (0, 0)
+
+
 def test_int8_layer_holds_its_codes_and_not_the_weights():
     import torch
     w = I.get("c1_tiny")
