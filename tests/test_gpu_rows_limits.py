@@ -286,3 +286,114 @@ def test_quantize_of_nearly_2_to_31_rows():
     assert int((s == float(one)).sum()) == n - 3
     assert q[-4:, 0].tolist() == [127, 127, -127, 0]
     assert s[-4:].tolist() == [one, np.float32(2) / np.float32(127), np.float32(4) / np.float32(127), 1.0]
+
+
+def _random_codes(rows, cols, pitch=None):
+    """int8 codes [rows, cols] of an LCG over the element's place, rows `pitch` bytes apart."""
+    import torch
+    q = torch.empty(rows, pitch or (cols + 15) // 16 * 16, dtype=torch.int8, device="cuda")
+    step = max(1, (1 << 28) // q.shape[1])
+    c = torch.arange(cols, device="cuda", dtype=torch.int32) * 7919
+    for r in range(0, rows, step):
+        i = torch.arange(r, min(r + step, rows), device="cuda", dtype=torch.int32)[:, None]
+        q[r:r + step, :cols] = (((i * 1103515245 + c) * 48271 >> 11) & 0xff).to(torch.int8)
+    return q[:, :cols]
+
+
+def _check_rows(out, a, sa, b, sb, rows, cols):
+    """Elements [rows] x [cols] of a product against float64 (integer sums below 2^53 are
+    exact): rounded to fp32, two scales, rounded to the output's type."""
+    import torch
+    got = out[rows][:, cols].double()
+    want = (a[rows].double() @ b[cols].double().t()) * sa[rows].double()[:, None] * \
+        sb[cols].double()
+    u = torch.finfo(out.dtype).eps / 2
+    assert torch.all((got - want).abs() <= (3 * 2.0 ** -24 * (1 + u) + u) * want.abs())
+
+
+def test_dispatch_int8_past_2_to_31_bytes():
+    import torch
+    T, d, E, k = 70000, 4096, 16, 8
+    dims = M.make_dims(T, d, E, k, 0, 0)
+    assert T * k * d > 1 << 31
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(T, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    idx = torch.rand(T, E, generator=g, device="cuda").topk(k, 1).indices.int().contiguous()
+    r, ws = M.alloc_sort(dims), M.alloc_sort_workspace(dims)
+    M.sort(dims, idx, r, ws)
+    q, s = M.alloc_codes(T * k, d)
+    M.dispatch_int8(dims, x, r["inv"], q, s, ws)
+    one, s1 = M.alloc_codes(T, d)
+    M.quantize_int8(x, one, s1)
+    assert M.read_device_status(ws) == (0, 0)
+    for t in range(0, T, 5000):
+        at = r["inv"][t:t + 5000].long()
+        assert torch.all(q[at] == one[t:t + 5000, None])
+        assert torch.all(s[at] == s1[t:t + 5000, None])
+
+
+@pytest.mark.parametrize("rows,N,K,pitch", [(600000, 64, 4000, None),   # a past 2^31 bytes
+                                            (300000, 8000, 16, None),   # out past 2^31 elements
+                                            (300000, 8001, 16, None),   # and rows off 16 bytes
+                                            (3000, 70, 100, 1 << 20)])  # rows far apart
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_product_past_2_to_31(rows, N, K, pitch, dtype):
+    import torch
+    a, b = _random_codes(rows, K, pitch), _random_codes(N, K, pitch)
+    g = torch.Generator(device="cuda").manual_seed(2)
+    sa, sb = (torch.rand(n, generator=g, device="cuda") + 0.5 for n in (rows, N))
+    out = torch.empty(rows, N, device="cuda", dtype={"bf16": torch.bfloat16, "f32": torch.float32}[dtype])
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    M.matmul_int8(a, sa, b, sb, out, ws)
+    assert M.read_device_status(ws) == (0, 0)
+    for r in (slice(0, 300), slice(rows // 2, rows // 2 + 300), slice(rows - 300, rows)):
+        _check_rows(out, a, sa, b, sb, r, slice(0, N))
+
+
+@pytest.mark.parametrize("G,rows,N,K", [(512, 28000, 80000, 16),  # out past 2^31 elements
+                                        (300, 900, 2000, 4096),   # b past 2^31 bytes
+                                        (300, 16, 2000, 4096),    # the same for a few rows
+                                        (4, 1, 1 << 26, 16)])
+def test_grouped_product_past_2_to_31(G, rows, N, K):
+    import torch
+    a, b = _random_codes(rows, K), _random_codes(G * N, K)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    sa, sb = (torch.rand(n, generator=g, device="cuda") + 0.5 for n in (rows, G * N))
+    # the last rows are the last group's; the first group has rows too where there are two
+    ends = torch.linspace(0, rows, G + 1).round().int()
+    if rows <= 16:
+        ends = torch.full((G + 1,), rows // 2, dtype=torch.int32)
+        ends[0], ends[G] = 0, rows
+    out = torch.empty(rows, N, device="cuda", dtype=torch.bfloat16)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    M.matmul_int8(a, sa, b.view(G, N, K), sb, out, ws, offsets=ends.cuda())
+    assert M.read_device_status(ws) == (0, 0)
+    for e in {0, G // 2, G - 1}:
+        lo, hi = int(ends[e]), min(int(ends[e + 1]), int(ends[e]) + 200)
+        for c in (slice(0, 2000), slice(N - 2000, N)):
+            _check_rows(out, a, sa, b[e * N:(e + 1) * N], sb[e * N:(e + 1) * N], slice(lo, hi), c)
+
+
+# ---------------------------------------------------------------- the int8 layer's shapes
+
+@pytest.mark.parametrize("T,d,E,k,F,Fs", [(130, 128, 60, 6, 192, 64),    # E off 16: CUDA-core router
+                                          (1100, 192, 48, 5, 64, 320),   # rows on 256-row tiles
+                                          (5, 64, 512, 16, 64, 0)])
+def test_int8_layer_shapes(T, d, E, k, F, Fs):
+    import torch
+    from tests.test_gpu_int8_layer import _reference
+    w = I.get("c1_tiny").with_(T=T, d_model=d, num_experts=E, num_experts_per_tok=k,
+                               moe_intermediate_size=F, shared_intermediate_size=Fs)
+    h = I.host_inputs(w)
+    dv = G.host_to_device(h)
+    layer = M.MoeLayer(dv, d, E, k, F, Fs, w.routed_scaling_factor, max_tokens=T // 2, int8=True)
+    y = layer.forward(dv["x"])  # more than it was made for: it grows
+    torch.cuda.synchronize()
+    assert layer.device_status() == (0, 0) and layer.max_tokens == T
+    idx, wt = (layer.routing[n].cpu().numpy().reshape(-1)[:T * k].reshape(T, k)
+               for n in ("topk_idx", "topk_w"))
+    ref = O.route(h["x"], h["w_router"], None, k)
+    G.check_routing(idx, wt, {"topk_idx": ref[0], "topk_w": ref[1], "scores": ref[2]}, k)
+    # as for the tiny layer: fp16 contributions, a bf16 sum, rarely a code across a border
+    want = _reference(w, h, idx, wt, h["x"])
+    assert np.linalg.norm(G.y_numpy(y) - want) <= 4e-3 * np.linalg.norm(want)
