@@ -14,8 +14,12 @@
 // end of a group, and outputs whose rows are no multiple of 16 bytes apart, are stored
 // from shared memory row by row.
 //
-// 16384 x 2048 x 4096: 88 us, 3.1e15 operations a second; 262144 rows of 256 experts:
-// gate/up with SwiGLU (N = 512, K = 2048) 485 us, down (N = 2048, K = 512) 350 us.
+// 16384 x 2048 x 4096: 88 to 92 us in a burst, 3.0e15 operations a second; 109 in a loop of a
+// second, which the power cap holds at 1.2 to 1.4 GHz.  262144 rows of 256 experts of unequal
+// size, one launch (in such a loop): gate/up with SwiGLU (N = 512, K = 2048) 485 us (600), down
+// (N = 2048, K = 512) 338 (416); of 1024 rows each 455 and 317, as one group 420 and 300.
+// At 96 registers a thread (the most for 576 threads) three of the six forms spill 4 to 12
+// bytes: fp32 without SwiGLU, bf16 and fp16 with it.
 //
 // Warps: 0 loads (TMA), 1 MMA issue (leader CTA), 2-17 epilogue, four to a quarter of
 // the lanes, each with a quarter of the columns.  Barriers as in moe_gemm_pair.cu's

@@ -128,10 +128,15 @@ __global__ void __launch_bounds__(kThreads)
 
 // One thread per item: up to k loads of each piece, kBatch of them in flight, summed in
 // slot order.  y may be add itself: a chunk is read before the same thread overwrites
-// it.  Bound by HBM: 16384 x 4096, top-16, bf16: 360 us, 6.7 TB/s, the gradient of the
-// copy (no weights) 325 us, 7.0 TB/s.  How many blocks fit on an SM decides that: 64
-// registers (weighted) and 56 (not), at 72 and 64 it was 374 and 331 us, at 56 and 48
-// they spill.
+// it.  Bound by HBM: 16384 x 4096, top-16, bf16: 358 us when repeated on the same rows (6.75
+// TB/s: some of them are still in L2), 370 to 394 on rows that change (6.1 to 6.5); the
+// gradient of the copy (no weights) 325 us, 7.0 TB/s.  How many blocks fit on an SM decides
+// that: 64 registers (weighted) and 56 (not).  At 64, 21 of the 27 weighted forms spill: 16
+// bytes for 16-bit inputs in chunks of eight, 68 in chunks of two, 8 to 48 in single elements;
+// none of the others does.  With 72 registers and no spills they are slower all the same: 368
+// against 358 us there, 368 against 352 (8192 x 4096 bf16, chunks of two), 1381 against 1154
+// (4097, single elements), 271 against 268 (fp32, single elements); fp32 in chunks of two 215
+// against 217.  At 56 and 48 the spills cost more.
 template <typename TI, typename TO, int N, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads, WEIGHTED ? 8 : 9)
     to_tokens_kernel(const TI *__restrict__ o, int64_t o_stride, const TI *add,
