@@ -49,7 +49,8 @@ def _build_lib(name, sources, extra=(), force=False, verbose=False):
     deps += [os.path.join(ROOT, "include", h) for h in ("moe.h", "moe_rows.h")]
     if not force and not _newer(out, deps):
         return out
-    cmd = [_nvcc(), *ARCH, *FLAGS, "-shared", "-o", out + ".tmp",
+    # (--threads 0: the sources side by side, one per host core)
+    cmd = [_nvcc(), *ARCH, *FLAGS, "--threads", "0", "-shared", "-o", out + ".tmp",
            *[os.path.join(CSRC, s) for s in sources], *extra]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)
