@@ -397,3 +397,28 @@ def test_int8_layer_shapes(T, d, E, k, F, Fs):
     # as for the tiny layer: fp16 contributions, a bf16 sum, rarely a code across a border
     want = _reference(w, h, idx, wt, h["x"])
     assert np.linalg.norm(G.y_numpy(y) - want) <= 4e-3 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("T", [1, 70])
+@pytest.mark.parametrize("Fs", [0, 128])
+def test_int8_layer_with_no_token_routed_and_with_rows_that_are_not_numbers(T, Fs):
+    import torch
+    w = I.get("c1_tiny").with_(T=T, shared_intermediate_size=Fs)
+    W = G.host_to_device(I.host_inputs(w))
+    layer = M.MoeLayer(W, w.d_model, w.E, w.k, w.F, w.Fs, max_tokens=T, int8=True)
+    x = W["x"]
+    y = layer.forward(x)
+    none = layer.forward(x, token_mask=torch.zeros(T, dtype=torch.uint8, device="cuda"))
+    assert layer.device_status() == (0, 0)
+    assert torch.isfinite(none).all() and int(layer.routing["offsets"][w.E]) == 0
+    assert (none == 0).all() == (Fs == 0)  # the shared expert alone
+    # a token that is not a number is its own loss only
+    bad = x.clone()
+    bad[T // 2, 3] = float("nan")
+    got = layer.forward(bad)
+    others = torch.arange(T, device="cuda") != T // 2
+    assert torch.isnan(got[T // 2]).all() and torch.equal(got[others], y[others])
+    bad[T // 2, 3] = float("inf")
+    got = layer.forward(bad)
+    assert torch.isnan(got[T // 2]).all() and torch.equal(got[others], y[others])
+    assert torch.equal(layer.forward(x), y) and layer.device_status() == (0, 0)
