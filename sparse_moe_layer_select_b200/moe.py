@@ -541,7 +541,7 @@ def prepare_int8(W, stream=None):
                           Q["s_gate_up_scale"][i * Fs:(i + 1) * Fs], stream=stream)
         Q["s_down"], Q["s_down_scale"] = rows(W["ws_down"])
     if stream is not None:
-        stream.synchronize()
+        torch.cuda.ExternalStream(stream.cuda_stream, device=dev).synchronize()
     bad = [n for n, t in Q.items() if n.endswith("_scale") and bool(torch.isnan(t).any())]
     if bad:
         raise MoeError(MOE_ERR_DEVICE_BOUNDS,
@@ -620,9 +620,9 @@ class MoeLayer:
 
             def buffers(rows, F):
                 # the activation stays in fp32 up to its codes: rounded to fp16 first, codes near
-                # a border would move.  The experts' outputs are rounded to fp16 (2^-11 of each
-                # at most, an eighth of the sum's own rounding to bf16), as the 16-bit layer's are: half
-                # the bytes that the product writes and the combine reads
+                # a border would move.  The experts' outputs are rounded to fp16, as the 16-bit
+                # layer's are (2^-11 of each at most, an eighth of the sum's own rounding to
+                # bf16): half the bytes for the product to write and the combine to read
                 b = {"h": new(rows, F, dtype=torch.float32),
                      "o": new(rows, c["d_model"], dtype=torch.float16)}
                 b["xq"], b["xs"] = alloc_codes(rows, c["d_model"], self.device)

@@ -1,5 +1,7 @@
 """Row operators, 8-bit products and the layers on them at their limits: batches smaller
 than the buffers were made for, row offsets past 2^31, scores that underflow."""
+import types
+
 import numpy as np
 import pytest
 
@@ -137,7 +139,8 @@ def test_int8_weights_with_an_infinity_or_nan_are_refused(name, at, value):
     w = I.get("c1_tiny")
     W = G.host_to_device(I.host_inputs(w))
     W[name][at] = value
-    for stream in (None, torch.cuda.Stream()):
+    raw = types.SimpleNamespace(cuda_stream=torch.cuda.Stream().cuda_stream)
+    for stream in (None, torch.cuda.Stream(), raw):
         torch.cuda.synchronize()
         with pytest.raises(M.MoeError) as e:
             M.prepare_int8(W, stream)
@@ -247,8 +250,6 @@ def test_swiglu_error_in_units_of_the_last_place(rows, grouped):
 
 def test_stream_arguments():
     """What is no stream of the tensors' device is refused, with no error left behind."""
-    import types
-
     import torch
     x = torch.ones(4, 64, device="cuda")
     q, s = M.alloc_codes(4, 64)
