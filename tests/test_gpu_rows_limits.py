@@ -448,3 +448,29 @@ def test_weight_gradient_of_long_rows(d, dtype):
     piece = min(64 // size, 8 * chunk)
     steps = piece + -(-d // (32 * piece)) + 6
     assert np.all(np.abs(f64(d_w)[:, 0] - want) <= steps * 2.0 ** -24 * want)
+
+
+# ---------------------------------------------------------------- more chunks than fit at once
+
+def test_sort_of_more_slots_than_one_launch_takes():
+    import torch
+    T, E, k = 400001, 60, 8  # 782 chunks of 4096: histogram and scatter in two launches
+    _, idx, _ = routing(T, E, k, 7, 0.1, True)
+    dims = M.make_dims(T, 8, E, k, 0, 0)
+    x = torch.arange(T, device="cuda", dtype=torch.float32)[:, None].expand(T, 8).contiguous()
+    x_perm = torch.full((T * k, 8), -1.0, device="cuda")
+    ws, out = M.alloc_sort_workspace(dims), M.alloc_sort(dims)
+    ws.fill_(0xFF)
+    M.sort(dims, dev(idx), out, ws, x=x, x_perm=x_perm)
+    assert M.read_device_status(ws) == (0, 0)
+    flat = idx.reshape(-1)
+    counts = np.bincount(flat[flat >= 0], minlength=E)
+    n = int(counts.sum())
+    perm = np.argsort(np.where(flat < 0, E, flat), kind="stable")[:n]
+    inv = np.full(T * k, -1)
+    inv[perm] = np.arange(n)
+    assert np.array_equal(out["counts"].cpu(), counts)
+    assert np.array_equal(out["offsets"].cpu(), np.concatenate([[0], np.cumsum(counts)]))
+    assert np.array_equal(out["perm"].cpu()[:n], perm)
+    assert np.array_equal(out["inv"].cpu().reshape(-1), inv)
+    assert np.array_equal(x_perm[:n, 3].cpu(), perm // k) and torch.all(x_perm[n:] == -1)
